@@ -10,6 +10,16 @@ or the device is not sm_100, calls raise.
     o, lse = attn_fwd_f32(q, k, v)                           # fp32 prefill
     o, lse = attn_decode_paged(q, k_pages, v_pages, block_table, seq_lens)
 
+and, around them, the rotation of queries and keys by their positions (with or
+without a norm of each head, and its gradients) and the 8-bit paged cache:
+
+    inv_freq, factor = rope_frequencies(128)
+    q, k = attn_norm_rope(q, k, q_weight, k_weight, positions, inv_freq)
+    attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_table,
+                           seq_lens, cu_q, max_q)
+    o, lse = attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table,
+                                   seq_lens, cu_q, max_q)
+
 Device-side failures (a corrupt block table, a bounded wait that ran out) are
 reported as ATTN_DEV_* bits: a decode given a ``workspace`` reports into that
 workspace (``decode_read_status``), every other call into the device's word
@@ -27,6 +37,9 @@ __all__ = [
     "attn_fwd", "attn_fwd_f32", "attn_decode_paged", "attn_decode_paged_noalloc",
     "attn_decode_paged_q8", "KV_FORMATS", "decode_workspace_bytes", "attn_bwd",
     "attn_prefill_paged",
+    "rope_frequencies", "attn_rope", "attn_norm_rope", "attn_norm_rope_bwd",
+    "norm_rope_bwd_workspace_bytes", "attn_kv_write_paged_q8", "attn_kv_read_paged_q8",
+    "attn_prefill_paged_q8", "prefill_q8_workspace_bytes",
     "bwd_workspace_bytes", "DECODE_NOALLOC_SCRATCH_BYTES",
     "device_status", "decode_read_status", "status_string", "version", "library", "LIB_PATH", "EXPORTED_SYMBOLS",
     "ATTN_DEV_BAD_PAGE", "ATTN_DEV_TIMEOUT", "ATTN_DEV_LAYOUT", "AttnError",
@@ -37,6 +50,10 @@ EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_f32", "attn_fwd_ext", "attn_fwd_f32_ex
                     "attn_bwd_workspace_bytes", "attn_bwd", "attn_prefill_paged",
                     "attn_decode_workspace_bytes",
                     "attn_decode_paged", "attn_decode_paged_noalloc", "attn_decode_paged_q8",
+                    "attn_kv_write_paged_q8", "attn_kv_read_paged_q8",
+                    "attn_prefill_q8_workspace_bytes", "attn_prefill_paged_q8",
+                    "attn_rope", "attn_norm_rope", "attn_norm_rope_bwd_workspace_bytes",
+                    "attn_norm_rope_bwd",
                     "attn_decode_read_status", "attn_device_status",
                     "attn_status_string", "attn_version")
 # Size of the library's fixed per-device scratch used by attn_decode_paged_noalloc.
@@ -47,9 +64,16 @@ ATTN_DEV_LAYOUT = 0x4
 # kv_format codes of attn_decode_paged_q8 and the torch dtypes accepted for each.
 KV_FORMATS = {"e4m3": 0, "int8": 1}
 _KV_DTYPES = {"e4m3": (torch.float8_e4m3fn, torch.uint8), "int8": (torch.int8,)}
+# Element types of the rotations and of attn_kv_read_paged_q8 (ATTN_DTYPE_*).
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3: "ATTN_ERR_CUDA"}
 
 _lib = None
+
+
+class _Strides(ctypes.Structure):
+    """attn_strides_t: elements between batch entries, heads and tokens."""
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
 
 
 class AttnError(RuntimeError):
@@ -104,6 +128,30 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.attn_decode_paged_q8.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, vp, vp, ci, ci, ci,
                                          ci, ci, ci, ci, cf, vp, ctypes.c_size_t, vp]
     lib.attn_decode_paged_q8.restype = ci
+    i64, st, sz = ctypes.c_int64, ctypes.POINTER(_Strides), ctypes.c_size_t
+    lib.attn_kv_write_paged_q8.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, ci, vp, vp,
+                                           vp, ci, ci, ci, ci, ci, ci, ci, ci, vp]
+    lib.attn_kv_write_paged_q8.restype = ci
+    lib.attn_kv_read_paged_q8.argtypes = [vp, vp, vp, vp, ci, vp, vp, vp, vp, vp, ci, ci, ci, ci,
+                                          ci, ci, ci, ci, ci, vp]
+    lib.attn_kv_read_paged_q8.restype = ci
+    lib.attn_prefill_q8_workspace_bytes.argtypes = [ci] * 8
+    lib.attn_prefill_q8_workspace_bytes.restype = sz
+    lib.attn_prefill_paged_q8.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, vp, vp, vp, ci, ci, ci,
+                                          ci, ci, ci, ci, ci, ci, cf, ci, vp, vp, sz, vp]
+    lib.attn_prefill_paged_q8.restype = ci
+    lib.attn_rope.argtypes = [vp, st, vp, st, vp, st, vp, st, vp, i64, vp, ci, ci, ci, ci, ci, ci,
+                              ci, ci, cf, ci, vp]
+    lib.attn_rope.restype = ci
+    lib.attn_norm_rope.argtypes = [vp, st, vp, vp, st, vp, st, vp, vp, st, vp, i64, vp, ci, ci, ci,
+                                   ci, ci, ci, ci, ci, cf, cf, vp]
+    lib.attn_norm_rope.restype = ci
+    lib.attn_norm_rope_bwd_workspace_bytes.argtypes = [ci] * 5
+    lib.attn_norm_rope_bwd_workspace_bytes.restype = sz
+    lib.attn_norm_rope_bwd.argtypes = [vp, st, vp, vp, st, vp, st, vp, vp, st, vp, vp, st, vp, st,
+                                       vp, vp, i64, vp, ci, ci, ci, ci, ci, ci, ci, ci, cf, cf, vp,
+                                       sz, vp]
+    lib.attn_norm_rope_bwd.restype = ci
     lib.attn_decode_read_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint)]
     lib.attn_decode_read_status.restype = ci
     lib.attn_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint), ci, vp]
@@ -517,6 +565,400 @@ def attn_decode_paged_noalloc(q, k_pages, v_pages, block_table, seq_lens,
             max_blocks, num_pages, float(scale), _stream(q))
     _raise(rc, "attn_decode_paged_noalloc")
     return out, lse
+
+
+def _q8_cache(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format):
+    """The 8-bit cache and the chunks of a call, checked against one another; shapes first, so
+    that they are reported the same way on any device."""
+    if kv_format not in KV_FORMATS:
+        raise ValueError("kv_format must be one of %s" % sorted(KV_FORMATS))
+    for name, t, nd in (("k_pages", k_pages, 4), ("v_pages", v_pages, 4),
+                        ("k_scales", k_scales, 2), ("v_scales", v_scales, 2),
+                        ("block_table", block_table, 2), ("seq_lens", seq_lens, 1),
+                        ("cu_q", cu_q, 1)):
+        _dims(t, name, nd)
+    num_pages, Hkv, page_size, d = k_pages.shape
+    S = seq_lens.shape[0]
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("v_pages must match k_pages, [num_pages, Hkv, page_size, d]")
+    if k_scales.shape != (num_pages, Hkv) or v_scales.shape != (num_pages, Hkv):
+        raise ValueError("scales must be [num_pages, Hkv]")
+    if block_table.shape[0] != S or cu_q.shape[0] != S + 1:
+        raise ValueError("block_table needs S rows and cu_q S+1 entries")
+    return num_pages, Hkv, page_size, d, S, block_table.shape[1]
+
+
+def _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format):
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype not in _KV_DTYPES[kv_format]:
+            raise TypeError("%s must be one of %s for kv_format %r"
+                            % (name, _KV_DTYPES[kv_format], kv_format))
+        _check(t, name, t.dtype, 4)
+    _check(k_scales, "k_scales", torch.float32, 2)
+    _check(v_scales, "v_scales", torch.float32, 2)
+    _check(block_table, "block_table", torch.int32, 2)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    _check(cu_q, "cu_q", torch.int32, 1)
+
+
+def attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
+                           max_q: int, kv_format: str = "e4m3"):
+    """Write a chunk's keys and values into the 8-bit cache, in place.
+
+    k, v [T,Hkv,d] bf16 token-major (sequence s: rows cu_q[s]..cu_q[s+1]-1, the
+    last tokens of its seq_lens[s], as for attn_prefill_paged_q8); they may be
+    views, such as slices of one projection's output, with consecutive elements
+    in a row.  Pages, scales, block_table, seq_lens and kv_format as for
+    attn_decode_paged_q8; cu_q [S+1] int32; max_q bounds every chunk length.
+    A page's scale grows with its tokens, and its earlier tokens are then rounded
+    to the new one; a page whose first slot is written starts afresh.  A page
+    that is written must belong to one sequence alone.
+    """
+    num_pages, Hkv, page_size, d, S, max_blocks = _q8_cache(
+        k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
+    for name, t in (("k", k), ("v", v)):
+        _dims(t, name, 3)
+        if tuple(t.shape[1:]) != (Hkv, d) or t.shape[0] != k.shape[0]:
+            raise ValueError("k and v must be [T, Hkv, d] as the pages are")
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
+    strides = []
+    for name, t in (("k", k), ("v", v)):
+        _rows(t, name, torch.bfloat16)
+        strides.append(_row_strides(t))
+    _same_device(k.device, v=v, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales,
+                 v_scales=v_scales, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q)
+    with torch.cuda.device(k.device):
+        rc = library().attn_kv_write_paged_q8(
+            k.data_ptr(), strides[0][1], strides[0][0], v.data_ptr(), strides[1][1], strides[1][0],
+            k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            KV_FORMATS[kv_format], block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S,
+            Hkv, k.shape[0], int(max_q), d, page_size, max_blocks, num_pages, _stream(k))
+    _raise(rc, "attn_kv_write_paged_q8")
+
+
+def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
+                          tokens: int, max_q: int, kv_format: str = "e4m3",
+                          dtype=torch.bfloat16, k=None, v=None):
+    """The last cu_q[s+1] - cu_q[s] tokens of each sequence out of the 8-bit cache.
+
+    Returns (k, v) [tokens,Hkv,d] of dtype (bfloat16 or float32), the element
+    scale * code; tokens is cu_q's last entry, or more: rows of no sequence are
+    not written.  max_q bounds every sequence's count.  Other arguments as for
+    attn_kv_write_paged_q8.
+    """
+    num_pages, Hkv, page_size, d, S, max_blocks = _q8_cache(
+        k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be torch.bfloat16 or torch.float32")
+    shape = (int(tokens), Hkv, d)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _dims(t, name, 3)
+            if tuple(t.shape) != shape:
+                raise ValueError("k and v must be [tokens, Hkv, d]")
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
+    k = torch.empty(shape, dtype=dtype, device=k_pages.device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=k_pages.device) if v is None else v
+    _check(k, "k", dtype, 3)
+    _check(v, "v", dtype, 3)
+    _same_device(k_pages.device, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales,
+                 block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, k=k, v=v)
+    with torch.cuda.device(k_pages.device):
+        rc = library().attn_kv_read_paged_q8(
+            k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            KV_FORMATS[kv_format], block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), _DTYPES[dtype], S, Hkv, int(tokens), int(max_q), d,
+            page_size, max_blocks, num_pages, _stream(k_pages))
+    _raise(rc, "attn_kv_read_paged_q8")
+    return k, v
+
+
+def prefill_q8_workspace_bytes(S: int, Hq: int, Hkv: int, T: int, max_q: int, d: int,
+                               max_blocks: int, page_size: int = 16) -> int:
+    return int(library().attn_prefill_q8_workspace_bytes(S, Hq, Hkv, T, max_q, d, max_blocks,
+                                                         page_size))
+
+
+def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
+                          max_q: int, kv_format: str = "e4m3", scale: float | None = None,
+                          window: int = 0, alibi_slopes=None, out=None, lse=None, workspace=None):
+    """Chunked prefill over the 8-bit paged cache.
+
+    q [T,Hq,d] bf16 token-major, cu_q, max_q, window and alibi_slopes as for
+    attn_prefill_paged; pages, scales and kv_format as for attn_decode_paged_q8.
+    Returns (O bf16 [T,Hq,d], L fp32 [T,Hq]); rows of no sequence are not
+    written.  ``workspace`` (uint8, at least prefill_q8_workspace_bytes(...) bytes)
+    is allocated when not given; calls that may run at the same time need one each.
+    """
+    num_pages, Hkv, page_size, d, S, max_blocks = _q8_cache(
+        k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
+    _dims(q, "q", 3)
+    T, Hq = q.shape[:2]
+    if q.shape[2] != d or Hq % Hkv != 0:
+        raise ValueError("q must be [T, Hq, d] with the pages' d and a multiple of their heads")
+    _decode_out_dims(q, T, Hq, out, lse)
+    if alibi_slopes is not None:
+        _dims(alibi_slopes, "alibi_slopes", 1)
+        if alibi_slopes.numel() != Hq:
+            raise ValueError("alibi_slopes needs one value per query head")
+    _check(q, "q", torch.bfloat16, 3)
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out, lse = _decode_outputs(q, T, Hq, out, lse)
+    slopes_ptr = None
+    if alibi_slopes is not None:
+        _check(alibi_slopes, "alibi_slopes", torch.float32, 1)
+        slopes_ptr = alibi_slopes.data_ptr()
+    need = prefill_q8_workspace_bytes(S, Hq, Hkv, T, int(max_q), d, max_blocks, page_size)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, 1)
+    _same_device(q.device, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales,
+                 block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, out=out, lse=lse,
+                 alibi_slopes=alibi_slopes, workspace=workspace)
+    with torch.cuda.device(q.device):
+        rc = library().attn_prefill_paged_q8(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
+            seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Hq, Hkv, T,
+            int(max_q), d, page_size, max_blocks, num_pages, float(scale), int(window), slopes_ptr,
+            workspace.data_ptr() if workspace is not None else None,
+            workspace.numel() if workspace is not None else 0, _stream(q))
+    _raise(rc, "attn_prefill_paged_q8")
+    return out, lse
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, original_length: int = 8192, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq, attention_factor) for the rotations: inv_freq float64 [rot/2] on device.
+
+    Pair i turns by base^(-2i/rot) radians a position.  For contexts ``factor``
+    times the original_length: "linear" divides every frequency by factor (all
+    positions are interpolated); "ntk" raises the base so that the slowest pair
+    alone is divided by factor and the fastest keeps its pace; "yarn" keeps pairs
+    that turn at least beta_fast times over the original length, divides those
+    that turn at most beta_slow times, blends in between, and asks for the
+    attention factor 0.1 ln(factor) + 1.
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    if not (math.isfinite(base) and base > 0 and math.isfinite(factor) and factor >= 1.0):
+        raise ValueError("base must be positive and factor at least 1")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    attention_factor = 1.0
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2.0))
+    freq = torch.pow(torch.tensor(base, dtype=torch.float64), -2.0 * i / rot)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        if not (beta_fast > beta_slow and original_length > 0):
+            raise ValueError("yarn needs beta_fast > beta_slow and a positive original_length")
+        turns = original_length * freq / (2.0 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        freq = freq * keep + freq / factor * (1.0 - keep)
+        attention_factor = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    return freq.to(device), attention_factor
+
+
+def _rows(t, name: str, dtype):
+    """A tensor of rows: any strides, but consecutive elements in a row."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.stride(-1) != 1:
+        raise ValueError("%s must have consecutive elements in its last dimension" % name)
+
+
+def _row_strides(t):
+    """(head, token) strides of a [T, H, d] tensor, 0 along an extent of one (where torch may
+    report any number)."""
+    return (t.stride(1) if t.shape[1] > 1 else 0, t.stride(0) if t.shape[0] > 1 else 0)
+
+
+def _strides(t):
+    if t.dim() == 3:
+        head, token = _row_strides(t)
+        return _Strides(0, head, token)
+    return _Strides(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+
+
+def _rope_args(q, k, positions, inv_freq, like_q, like_k):
+    """Shapes, types and devices of a rotation's tensors.  like_q, like_k: names and tensors
+    (or None) that must look like q and k.  Returns B, Hq, Hkv, N, d and the position stride."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    nd = q.dim()
+    if nd not in (3, 4):
+        raise ValueError("q must be [B, Hq, N, d] or token-major [T, Hq, d], got shape %s"
+                         % (tuple(q.shape),))
+    if k is not None:
+        _dims(k, "k", nd)
+        if nd == 4 and (k.shape[0], k.shape[2], k.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]):
+            raise ValueError("k must be [B, Hkv, N, d] matching q %s" % (tuple(q.shape),))
+        if nd == 3 and (k.shape[0], k.shape[2]) != (q.shape[0], q.shape[2]):
+            raise ValueError("k must be [T, Hkv, d] matching q %s" % (tuple(q.shape),))
+    elif any(t is not None for _, t in like_k):
+        raise ValueError("%s given without k" % like_k[0][0])
+    if not isinstance(positions, torch.Tensor) or not isinstance(inv_freq, torch.Tensor):
+        raise TypeError("positions and inv_freq must be torch.Tensors")
+    B, N = (1, q.shape[0]) if nd == 3 else (q.shape[0], q.shape[2])
+    if tuple(positions.shape) != (N,) and (nd == 3 or tuple(positions.shape) != (B, N)):
+        raise ValueError("positions must be [T] or [N], or [B, N] with a batch")
+    _dims(inv_freq, "inv_freq", 1)
+    if not 1 <= inv_freq.shape[0] <= q.shape[-1] // 2:
+        raise ValueError("inv_freq needs one value per pair, at most d/2")
+    for like, ref, what in ((like_q, q, "q"), (like_k, k, "k")):
+        for name, t in like:
+            if t is not None:
+                _dims(t, name, nd)
+                if t.shape != ref.shape:
+                    raise ValueError("%s must have %s's shape" % (name, what))
+    if q.dtype not in _DTYPES:
+        raise TypeError("q must be bfloat16 or float32, got %s" % q.dtype)
+    _rows(q, "q", q.dtype)
+    if k is not None:
+        _rows(k, "k", q.dtype)
+    for name, t in like_q + like_k:
+        if t is not None:
+            _rows(t, name, q.dtype)
+    _check(positions, "positions", torch.int32, positions.dim())
+    _check(inv_freq, "inv_freq", torch.float64, 1)
+    _same_device(q.device, k=k, positions=positions, inv_freq=inv_freq,
+                 **dict(like_q + like_k))
+    Hkv = 0 if k is None else k.shape[1]
+    return B, q.shape[1], Hkv, N, q.shape[-1], N if positions.dim() == 2 else 0
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ref(t):
+    return None if t is None else ctypes.byref(_strides(t))
+
+
+def _empty_rows(t):
+    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def attn_rope(q, k, positions, inv_freq, interleaved: bool = False, attention_factor: float = 1.0,
+              transpose: bool = False, q_out=None, k_out=None):
+    """Rotary positions of q and k: returns (q_out, k_out).
+
+    q [B,Hq,N,d] and k [B,Hkv,N,d], or token-major [T,Hq,d] and [T,Hkv,d]; bf16 or
+    float32; k may be None.  They may be views (slices of one projection's
+    output, transposed layouts) with consecutive elements in a row; given outputs
+    too, and an output may be its input.  positions int32 [N] or [B,N] ([T]);
+    inv_freq float64 [rot/2] (see rope_frequencies): the first rot elements of
+    each row turn, pairs (i, i + rot/2) or, interleaved, (2i, 2i+1), times
+    attention_factor; the others pass.  transpose applies the transposed map, the
+    gradient of the other.
+    """
+    B, Hq, Hkv, N, d, pos_stride = _rope_args(q, k, positions, inv_freq, [("q_out", q_out)],
+                                              [("k_out", k_out)])
+    q_out = _empty_rows(q) if q_out is None else q_out
+    k_out = _empty_rows(k) if k_out is None else k_out
+    with torch.cuda.device(q.device):
+        rc = library().attn_rope(_ptr(q), _ref(q), _ptr(q_out), _ref(q_out), _ptr(k), _ref(k),
+                                 _ptr(k_out), _ref(k_out), positions.data_ptr(), pos_stride,
+                                 inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N, d,
+                                 2 * inv_freq.shape[0], int(bool(interleaved)),
+                                 float(attention_factor), int(bool(transpose)), _stream(q))
+    _raise(rc, "attn_rope")
+    return q_out, k_out
+
+
+def _norm_weights(q, k, q_weight, k_weight):
+    if (k is None) != (k_weight is None):
+        raise ValueError("k and k_weight go together")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None or name == "q_weight":
+            _dims(t, name, 1)
+            if t.shape[0] != q.shape[-1]:
+                raise ValueError("%s must be [d]" % name)
+            _check(t, name, q.dtype, 1)
+    _same_device(q.device, q_weight=q_weight, k_weight=k_weight)
+
+
+def attn_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6,
+                   interleaved: bool = False, attention_factor: float = 1.0, q_out=None,
+                   k_out=None):
+    """RMS norm of every head's row, times its weights, then attn_rope: (q_out, k_out).
+
+    q_weight, k_weight [d] of q's dtype, shared by the heads (k_weight None without
+    k).  Other arguments as for attn_rope.
+    """
+    B, Hq, Hkv, N, d, pos_stride = _rope_args(q, k, positions, inv_freq, [("q_out", q_out)],
+                                              [("k_out", k_out)])
+    _norm_weights(q, k, q_weight, k_weight)
+    q_out = _empty_rows(q) if q_out is None else q_out
+    k_out = _empty_rows(k) if k_out is None else k_out
+    with torch.cuda.device(q.device):
+        rc = library().attn_norm_rope(_ptr(q), _ref(q), _ptr(q_weight), _ptr(q_out), _ref(q_out),
+                                      _ptr(k), _ref(k), _ptr(k_weight), _ptr(k_out), _ref(k_out),
+                                      positions.data_ptr(), pos_stride, inv_freq.data_ptr(),
+                                      _DTYPES[q.dtype], B, Hq, Hkv, N, d, 2 * inv_freq.shape[0],
+                                      int(bool(interleaved)), float(attention_factor), float(eps),
+                                      _stream(q))
+    _raise(rc, "attn_norm_rope")
+    return q_out, k_out
+
+
+def norm_rope_bwd_workspace_bytes(B: int, Hq: int, Hkv: int, N: int, d: int) -> int:
+    return int(library().attn_norm_rope_bwd_workspace_bytes(B, Hq, Hkv, N, d))
+
+
+def attn_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, positions, inv_freq,
+                       eps: float = 1e-6, interleaved: bool = False,
+                       attention_factor: float = 1.0, dq=None, dk=None, dq_weight=None,
+                       dk_weight=None, workspace=None):
+    """Gradients of attn_norm_rope: (dq, dk, dq_weight, dk_weight).
+
+    q, k and the options as given to attn_norm_rope; dq_out, dk_out the gradients of
+    its outputs.  dq, dk have q's dtype (dq may be dq_out or q); dq_weight,
+    dk_weight are float32 [d].  Without k its parts are None.
+    """
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    if dq_out is None:
+        raise TypeError("dq_out must be a torch.Tensor")
+    B, Hq, Hkv, N, d, pos_stride = _rope_args(q, k, positions, inv_freq,
+                                              [("dq_out", dq_out), ("dq", dq)],
+                                              [("dk_out", dk_out), ("dk", dk)])
+    _norm_weights(q, k, q_weight, k_weight)
+    dq = _empty_rows(q) if dq is None else dq
+    dk = _empty_rows(k) if dk is None else dk
+    if dq_weight is None:
+        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+    if dk_weight is None and k is not None:
+        dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if t is not None:
+            _check(t, name, torch.float32, 1)
+            if t.shape[0] != d or k is None and name == "dk_weight":
+                raise ValueError("%s must be [d], and None without k" % name)
+    need = norm_rope_bwd_workspace_bytes(B, Hq, Hkv, N, d)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check(workspace, "workspace", torch.uint8, 1)
+    _same_device(q.device, dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace)
+    with torch.cuda.device(q.device):
+        rc = library().attn_norm_rope_bwd(
+            _ptr(q), _ref(q), _ptr(q_weight), _ptr(dq_out), _ref(dq_out), _ptr(dq), _ref(dq),
+            _ptr(dq_weight), _ptr(k), _ref(k), _ptr(k_weight), _ptr(dk_out), _ref(dk_out),
+            _ptr(dk), _ref(dk), _ptr(dk_weight), positions.data_ptr(), pos_stride,
+            inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N, d, 2 * inv_freq.shape[0],
+            int(bool(interleaved)), float(attention_factor), float(eps), workspace.data_ptr(),
+            workspace.numel(), _stream(q))
+    _raise(rc, "attn_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
 
 
 def decode_read_status(workspace: torch.Tensor) -> int:

@@ -66,6 +66,47 @@ attn_status_t launch_decode_paged_q8(const void *q, const void *k_pages, const v
                                      int num_pages, float scale, void *workspace,
                                      cudaStream_t stream);
 
+// Chunked prefill over the 8-bit pages; workspace: the parts of a call whose keys
+// are split (0 bytes where it is not).
+size_t prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q, int d, int max_blocks);
+attn_status_t launch_prefill_paged_q8(const void *q, const void *k_pages, const void *v_pages,
+                                      const float *k_scales, const float *v_scales, int kv_format,
+                                      const int *block_table, const int *seq_lens, const int *cu_q,
+                                      void *o, float *lse, int S, int Hq, int Hkv, int T, int max_q,
+                                      int d, int max_blocks, int num_pages, float scale, int window,
+                                      const float *slopes, void *workspace, cudaStream_t stream,
+                                      unsigned *status);
+
+// Writing a chunk's keys and values into the 8-bit pages (strides: k's token and
+// head stride, then v's, in elements) and reading a range of tokens back.
+attn_status_t launch_kv_write_q8(const void *k, const void *v, const long long (&strides)[4],
+                                 void *k_pages, void *v_pages, float *k_scales, float *v_scales,
+                                 int kv_format, const int *block_table, const int *seq_lens,
+                                 const int *cu_q, int S, int Hkv, int T, int max_q, int d,
+                                 int max_blocks, int num_pages, cudaStream_t stream,
+                                 unsigned *status);
+attn_status_t launch_kv_read_q8(const void *k_pages, const void *v_pages, const float *k_scales,
+                                const float *v_scales, int kv_format, const int *block_table,
+                                const int *seq_lens, const int *cu_q, void *k, void *v, int dtype,
+                                int S, int Hkv, int T, int max_q, int d, int max_blocks,
+                                int num_pages, cudaStream_t stream, unsigned *status);
+
+// Rotary positions (op 0), a norm of each head before them (1), the gradient of
+// that (2).  One side is q, the other k (H = 0: none).
+struct RopeSide {
+  const void *x, *dy;
+  void *y;        // output, or dx
+  const void *w;  // norm weights
+  float *dw;
+  attn_strides_t x_st, y_st, dy_st;
+  int H;
+};
+size_t norm_rope_bwd_workspace_bytes(long long tokens, int Hq, int Hkv, int d);
+attn_status_t launch_rope(const RopeSide &q, const RopeSide &k, const int *positions,
+                          long long pos_stride, const double *inv_freq, int dtype, int op, int B,
+                          int N, int d, int rot, int interleaved, float factor, int transpose,
+                          float eps, void *workspace, cudaStream_t stream);
+
 // Backward: workspace (L*log2e and rowsum(dO*O) per query row, padded to whole
 // 128-row tiles) and the three-kernel launch.
 size_t bwd_workspace_bytes(int B, int Hq, int N);

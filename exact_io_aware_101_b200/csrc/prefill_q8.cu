@@ -1,0 +1,929 @@
+// prefill_q8.cu -- attention of a chunk of new tokens over an 8-bit paged cache.
+//
+// What it computes: the chunked prefill of prefill_sm100.cu ("Phase 08" page,
+// Concepts: chunked prefill, paged attention; Lab 03 step 4) over the 8-bit
+// cache of decode_q8.cu: the element is scale * code, one float32 scale per
+// (page, K/V head) of K and of V, and chunk query t of a sequence, at position
+// ctx + t, sees keys 0 .. ctx + t (less those behind a window).
+//
+// How it maps to sm_100a.  The two products run on tcgen05 (kind::f16, f16
+// operands, f32 accumulators in TMEM), which takes its B operand from shared
+// memory in 16 bits, so the codes are widened on the way there.  Doing that in
+// the kernel keeps the cache's traffic at one byte per element; widening the
+// cache in a pass of its own would write and read twice that.
+//  * Rows: the query heads that share a K/V head are rows of one tile.  A CTA
+//    has two tiles of 128 rows, each floor(128 / G) tokens by G heads (G = Hq /
+//    Hkv, or a divisor of it up to 128), so a widened tile serves the whole
+//    group, and a chunk of a few tokens fills a tile instead of G of them.
+//  * 16 warps in four warpgroups:
+//      warp 0       allocates TMEM and issues every tcgen05.mma;
+//      warps 4-7    widen: each takes two pages of a 128-key tile, reads their
+//                   codes with 16-byte loads one tile ahead of their use,
+//                   converts them and stores them into a ring of NST slots in
+//                   the 128-byte-swizzled layout that the MMAs read;
+//      warps 8-11   softmax, correction and epilogue of tile 0, warps 12-15 of
+//                   tile 1; before that they bring the tiles' queries to f16.
+//    Measured on the chunked workload (16 chunks of 512, Hq = 32, Hkv = 8, d =
+//    128): see the table of operators.
+//  * Exactness.  Codes are exact in f16.  Queries are scaled by a power of two
+//    per row before rounding to f16, exact for elements within 2^28 of the
+//    row's largest.  The K scale multiplies the f32 scores, per page.  The V
+//    scale multiplies the code on its way to f16, rounded once: v = fma(code,
+//    hi, code * lo) with hi + lo the scale to 22 bits, relative to a power of
+//    two just above the largest V scale of the CTA's pages.  (A page whose V
+//    scale is under 2^-19 of that largest one loses bits of its own values.)
+//    P is rounded to f16 (2^-11 of each, against bf16's 2^-8 of the output).
+//  * Few rows and long keys: when the row tiles alone leave SMs idle, each
+//    tile's keys are split over several CTAs, which write normalised partials
+//    and their log2-sum-exps to the workspace; a second kernel, scheduled
+//    behind the first, joins them.
+//  * NaN behind the mask: a masked score is replaced, whatever it was.  In the
+//    P V product a zero weight would not cancel a NaN value, so in tiles that
+//    some row sees only in part such values enter as zeros and are noted by
+//    key; a row that does see a noted key gets NaN.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace exattn {
+namespace {
+
+constexpr int BM = 128;  // rows of a tile
+constexpr int BN = 128;  // keys of a tile
+constexpr int kPage = 16;
+constexpr int kPagesPerTile = BN / kPage;
+constexpr int NUM_THREADS = 512;
+constexpr int kRegsMma = 48, kRegsWiden = 112, kRegsSoft = 176;
+static_assert(128 * (kRegsMma + kRegsWiden + 2 * kRegsSoft) <= NUM_THREADS * 128,
+              "setmaxnreg split must fit the block's launch registers");
+constexpr int kRankMax = NUM_THREADS;   // sequences ranked by length
+constexpr int CHUNK_BYTES = 128 * 128;  // one 128-row x 128-byte swizzle column block
+constexpr int kSMs = 148;
+constexpr int kScaleRing = 8;  // tiles whose K scales are kept (four would do, see issue order)
+constexpr int kEdge = 4;       // tiles that a row may see in part, at either end of the walk
+
+template <int D>
+struct Cfg {
+  static constexpr int TILE_BYTES = BM * D * 2;  // a Q, K or V tile in f16
+  static constexpr int NST = (D == 64) ? 8 : 4;  // ring slots
+  static constexpr int RING_OFF = 2 * TILE_BYTES;
+  static constexpr int BAR_OFF = RING_OFF + NST * TILE_BYTES;
+  static constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;  // + 1 KB align slack
+  static constexpr uint32_t IDESC_QK =  // as idesc_bf16_f32, with both operand formats 0 (f16)
+      idesc_bf16_f32(BM, BN, false, false) & ~((7u << 7) | (7u << 10));
+  static constexpr uint32_t IDESC_PV =
+      idesc_bf16_f32(BM, D, false, true) & ~((7u << 7) | (7u << 10));
+};
+
+struct Shared {
+  uint64_t full[8];
+  uint64_t empty[8];
+  uint64_t q_full[2];
+  uint64_t s_full[2];
+  uint64_t p_full[2];
+  uint64_t o_full[2];
+  uint64_t mma_done;
+  alignas(16) float k_scale[kScaleRing][kPagesPerTile];
+  unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with a NaN or infinite value
+  unsigned v_top;                      // largest finite |V scale| of the CTA's pages, as bits
+  int any_bad;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Shared) <= 1024, "fits behind the ring");
+
+struct Params {
+  const __nv_bfloat16 *q;
+  const uint8_t *k_pages, *v_pages;
+  const float *k_scales, *v_scales;
+  const int *block_table, *seq_lens, *cu_q;
+  __nv_bfloat16 *o;
+  float *lse;
+  float *o_part, *l2_part;  // nsplit > 1: [T][Hq][nsplit][D] and [T][Hq][nsplit]
+  const float *slopes;
+  unsigned *status;
+  int S, Hq, Hkv, T, max_q, max_blocks, num_pages;
+  int heads;      // query heads per CTA (rows of a token)
+  int tokens;     // tokens per tile: floor(128 / heads)
+  int pairs;      // tile pairs for max_q tokens
+  int nsplit;
+  float scale_log2;
+  int window;
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+// Shared-memory stores of this thread become visible to the tensor core's reads.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Four codes of a word -> two f16x2, exactly (element 0 in the low half of a).
+template <int FMT>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &a, uint32_t &b) {
+  if constexpr (FMT == ATTN_KV_E4M3) {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+  } else {
+    // The byte, sign flipped, in the mantissa of 1024 is code + 1152.
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = as_h2(0x64806480u);
+    a = as_u32(__hsub2(as_h2(prmt(u, 0x64646464u, 0x4140u)), bias));
+    b = as_u32(__hsub2(as_h2(prmt(u, 0x64646464u, 0x4342u)), bias));
+  }
+}
+
+// A thread's whole score row, in two loads (ptxas holds one instruction's
+// registers to the launch's 128 a thread).
+__device__ __forceinline__ void load_row(uint32_t addr, uint32_t (&sv)[128]) {
+  tmem_ld64(addr, *reinterpret_cast<uint32_t(*)[64]>(sv));
+  tmem_ld64(addr + 64, *reinterpret_cast<uint32_t(*)[64]>(sv + 64));
+}
+__device__ __forceinline__ void row_loaded(uint32_t (&sv)[128]) {
+  tmem_ld_wait64(*reinterpret_cast<uint32_t(*)[64]>(sv));
+  tmem_ld_wait64(*reinterpret_cast<uint32_t(*)[64]>(sv + 64));
+}
+
+// 32 columns cc*32 .. of one thread's score row -> 16 f16 pairs of P = 2^(s*c -
+// m), c the multiplier of the columns' page, and their part of the row sum.
+__device__ __forceinline__ void exp_chunk(const uint32_t (&sv)[128], int cc, float c0, float c1,
+                                          float m, uint32_t *pk, float2 &sum_a, float2 &sum_b) {
+  const float2 nm2 = make_float2(-m, -m);
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const int col = cc * 32 + i;
+    const float c = i < 16 ? c0 : c1;
+    const float2 c2 = make_float2(c, c);
+    const float2 x0 = fma2(make_float2(__uint_as_float(sv[col]), __uint_as_float(sv[col + 1])), c2, nm2);
+    const float2 x1 = fma2(make_float2(__uint_as_float(sv[col + 2]), __uint_as_float(sv[col + 3])), c2, nm2);
+    const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
+    const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
+    sum_a = add2(sum_a, p0);
+    sum_b = add2(sum_b, p1);
+    pk[i >> 1] = pack_f16x2(p0.x, p0.y);
+    pk[(i >> 1) + 1] = pack_f16x2(p1.x, p1.y);
+  }
+}
+
+// A sequence's chunk: rows q0 .. q0 + nq - 1, its last token the n-th.  False
+// where the lengths do not fit.
+struct Chunk {
+  int q0, nq, n, ctx;
+};
+__device__ __forceinline__ bool chunk_of(const Params &p, int s, Chunk &c) {
+  c.q0 = p.cu_q[s];
+  const int q1 = p.cu_q[s + 1];
+  c.n = p.seq_lens[s];
+  const long long nq = static_cast<long long>(q1) - c.q0;  // (a corrupt pair could wrap)
+  c.nq = static_cast<int>(nq);
+  c.ctx = c.n - c.nq;
+  return c.q0 >= 0 && nq >= 0 && nq <= p.max_q && q1 <= p.T && c.n >= nq &&
+         c.n <= static_cast<long long>(p.max_blocks) * kPage;
+}
+
+// A tile's raw codes in flight: each widening warp's two pages, 16 bytes a lane.
+template <int D>
+struct Raw {
+  static constexpr int RPP = 512 / D;          // rows per 512-byte pass
+  static constexpr int PASSES = kPage / RPP;   // passes per page
+  uint4 w[2][PASSES];
+  float scale[2];
+};
+
+template <int D, int FMT, bool kAlibi>
+__global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params p) {
+  using C = Cfg<D>;
+  grid_dependents_launch();  // the joining kernel may be scheduled behind this grid
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sRing = smem + C::RING_OFF;
+  Shared *sh = reinterpret_cast<Shared *>(smem + C::BAR_OFF);
+  volatile int *abort_flag = &sh->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- work item: longest sequence first, its last (heaviest) pair first,
+  // so that the last wave holds the short ones.  Past kRankMax sequences the
+  // order stays as given.
+  const int groups = p.Hq / p.heads;  // head groups of a token
+  const int per_pair = groups * p.nsplit;
+  const int per_seq = p.pairs * per_pair;
+  const int lin = static_cast<int>(blockIdx.x);
+  const int rank_of = lin / per_seq, rem = lin - rank_of * per_seq;
+  const int pair = p.pairs - 1 - rem / per_pair;
+  const int group = (rem % per_pair) / p.nsplit, part = rem % p.nsplit;
+  int seq = rank_of;
+  if (p.S > 1 && p.S <= kRankMax) {
+    __shared__ int s_len[kRankMax];
+    __shared__ int s_seq;
+    const int t = static_cast<int>(threadIdx.x);
+    if (t < p.S) s_len[t] = p.seq_lens[t];
+    __syncthreads();
+    if (t < p.S) {
+      const int nt = s_len[t];
+      int rank = 0;
+      for (int u = 0; u < p.S; ++u) rank += (s_len[u] > nt) || (s_len[u] == nt && u < t);
+      if (rank == rank_of) s_seq = t;
+    }
+    __syncthreads();
+    seq = s_seq;
+  }
+  Chunk ck;
+  if (!chunk_of(p, seq, ck)) {
+    if (threadIdx.x == 0 && pair == 0 && group == 0 && part == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
+    return;
+  }
+  const int tok0 = pair * 2 * p.tokens;  // first token of tile 0
+  if (tok0 >= ck.nq) return;
+  const int h0 = group * p.heads;                  // first query head
+  const int hkv = h0 / (p.Hq / p.Hkv);
+  const bool rows1 = tok0 + p.tokens < ck.nq;      // tile 1 has rows
+  // Key tiles [js_t, je_t) of each row tile.
+  int je0 = (ck.ctx + min(tok0 + p.tokens, ck.nq) - 1) / BN + 1;
+  int je1 = rows1 ? (ck.ctx + min(tok0 + 2 * p.tokens, ck.nq) - 1) / BN + 1 : 0;
+  int js0 = p.window > 0 ? max(0, ck.ctx + tok0 - p.window + 1) / BN : 0;
+  int js1 = p.window > 0 && rows1 ? max(0, ck.ctx + tok0 + p.tokens - p.window + 1) / BN : 0;
+  // Tiles from edge_hi on, and (with a window) those before edge_lo, hold keys
+  // that some row of this CTA does not see.  At most kEdge of each: the rows
+  // span at most 256 positions.
+  const int edge_hi = (ck.ctx + tok0 + 1) / BN;
+  const int edge_0 = js0;
+  int jlo = js0, jhi = max(je0, je1);
+  if (p.nsplit > 1) {  // this CTA's part of them
+    const int n = jhi - jlo, first = jlo;
+    jlo = first + static_cast<int>(static_cast<long long>(n) * part / p.nsplit);
+    jhi = first + static_cast<int>(static_cast<long long>(n) * (part + 1) / p.nsplit);
+    js0 = max(js0, jlo);
+    js1 = max(js1, jlo);
+    je0 = min(je0, jhi);
+    je1 = min(je1, jhi);
+  }
+
+  // ---- every page of those tiles must be in the pool; and their largest V scale.
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(&sh->full[i], 128);
+      mbar_init(&sh->empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh->q_full[t], BM);
+      mbar_init(&sh->s_full[t], 1);
+      mbar_init(&sh->p_full[t], BM);
+      mbar_init(&sh->o_full[t], 1);
+    }
+    mbar_init(&sh->mma_done, 1);
+    sh->abort_flag = 0;
+    sh->any_bad = 0;
+    sh->v_top = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 2 * kEdge * (BN / 32)) (&sh->v_bad[0][0])[threadIdx.x] = 0;
+  __syncthreads();
+  {
+    const int pg_end = min(jhi * kPagesPerTile, (ck.n + kPage - 1) / kPage);
+    bool bad = false;
+    unsigned top = 0;
+    for (int i = jlo * kPagesPerTile + static_cast<int>(threadIdx.x); i < pg_end; i += NUM_THREADS) {
+      const int pid = p.block_table[static_cast<size_t>(seq) * p.max_blocks + i];
+      if (pid < 0 || pid >= p.num_pages) {
+        bad = true;
+      } else {
+        const unsigned u = __float_as_uint(p.v_scales[static_cast<size_t>(pid) * p.Hkv + hkv]) & 0x7fffffffu;
+        if (u < 0x7f800000u) top = max(top, u);
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0 && top) atomicMax(&sh->v_top, top);
+    if (__syncthreads_or(bad) || jlo >= jhi) {
+      // NaN rows for a bad page; nothing (weight zero) for a part without keys.
+      const bool none = jlo >= jhi;
+      if (!none && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
+      const float fill = none ? 0.f : NAN;
+      const int ntok = min(2 * p.tokens, ck.nq - tok0);
+      for (int i = threadIdx.x; i < ntok * p.heads * D; i += NUM_THREADS) {
+        const int c = i % D, r = i / D;
+        const size_t row = static_cast<size_t>(ck.q0 + tok0 + r / p.heads) * p.Hq + h0 + r % p.heads;
+        if (p.nsplit == 1) {
+          p.o[row * D + c] = __float2bfloat16_rn(fill);
+          if (c == 0) p.lse[row] = fill;
+        } else {
+          p.o_part[(row * p.nsplit + part) * D + c] = fill;
+          if (c == 0) p.l2_part[row * p.nsplit + part] = none ? -INFINITY : fill;
+        }
+      }
+      return;
+    }
+  }
+  if (warp == 0) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  // V is widened relative to 2^v_exp: the largest scale lands in [2^5, 2^6), so
+  // that 448 of it stays below f16's largest.
+  int v_exp = 0;
+  if (sh->v_top) v_exp = max(-120, static_cast<int>(sh->v_top >> 23) - 127 - 5);
+
+  if (warp < 4) {
+    // ================================================================== MMA
+    regs_dec<kRegsMma>();
+    if (warp == 0 && lane == 0) {
+      const uint32_t ring_base = smem_u32(sRing);
+      auto slot_of = [](int i) { return i % C::NST; };
+      auto wait_full = [&](int i) {
+        return mbar_wait(&sh->full[i % C::NST], (i / C::NST) & 1, abort_flag, p.status);
+      };
+      const uint64_t qdesc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t kdesc0 = sdesc_sw128(ring_base, 16, 1024);
+      const uint64_t vdesc0 = sdesc_sw128(ring_base, CHUNK_BYTES, 1024);
+      auto issue_s = [&](int t, int kidx) {  // S_t = Q_t K^T
+        const uint64_t qd = qdesc0 + ((t * C::TILE_BYTES) >> 4);
+        const uint64_t kd = kdesc0 + ((slot_of(kidx) * C::TILE_BYTES) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * CHUNK_BYTES + (ks & 3) * 32) >> 4;
+          mma_ss(tmem + t * 128, qd + off, kd + off, C::IDESC_QK, ks > 0);
+        }
+        tc_commit(&sh->s_full[t]);
+      };
+      auto issue_pv = [&](int t, int vidx, bool acc) {  // O_t (+)= P_t V
+        const uint64_t vd = vdesc0 + ((slot_of(vidx) * C::TILE_BYTES) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < BN / 16; ++ks)
+          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4),
+                 C::IDESC_PV, (acc || ks > 0) ? 1u : 0u);
+        tc_commit(&sh->o_full[t]);
+      };
+      // Tile j sits at ring index 2 * (j - jlo) (K) and one behind (V).
+      auto has = [&](int t, int j) {
+        return t == 0 ? (j >= js0 && j < je0) : (j >= js1 && j < je1);
+      };
+      bool ok = wait_full(0);
+      if (ok && js0 < je0) ok = mbar_wait(&sh->q_full[0], 0, abort_flag, p.status);
+      if (ok && js1 < je1) ok = mbar_wait(&sh->q_full[1], 0, abort_flag, p.status);
+      if (ok) {
+        tc_fence_after();
+        if (has(0, jlo)) issue_s(0, 0);
+        if (has(1, jlo)) issue_s(1, 0);
+        tc_commit(&sh->empty[slot_of(0)]);
+      }
+      for (int rj = 0; ok && rj < jhi - jlo; ++rj) {
+        const int j = jlo + rj;
+        const bool more = j + 1 < jhi;
+        if (!(ok = wait_full(2 * rj + 1))) break;
+        if (more && !(ok = wait_full(2 * rj + 2))) break;
+        if (has(0, j)) {
+          if (!(ok = mbar_wait(&sh->p_full[0], (j - js0) & 1, abort_flag, p.status))) break;
+          tc_fence_after();
+          issue_pv(0, 2 * rj + 1, j > js0);
+        }
+        // P_t(j) lies over S_t: the MMAs of one thread run in order, so S_t(j+1)
+        // is written only after P_t(j) has been read.
+        if (more && has(0, j + 1)) issue_s(0, 2 * rj + 2);
+        if (has(1, j)) {
+          if (!(ok = mbar_wait(&sh->p_full[1], (j - js1) & 1, abort_flag, p.status))) break;
+          tc_fence_after();
+          issue_pv(1, 2 * rj + 1, j > js1);
+        }
+        tc_commit(&sh->empty[slot_of(2 * rj + 1)]);
+        if (more && has(1, j + 1)) issue_s(1, 2 * rj + 2);
+        if (more) tc_commit(&sh->empty[slot_of(2 * rj + 2)]);
+      }
+      // Every MMA issued above must finish before TMEM is released.
+      tc_commit(&sh->mma_done);
+      mbar_wait_drain(&sh->mma_done, 0, p.status);
+    }
+  } else if (warp < 8) {
+    // =============================================================== widening
+    regs_dec<kRegsWiden>();
+    using R = Raw<D>;
+    const int w = warp - 4;
+    constexpr int LPR = D / 16;  // lanes per row
+    const int row = lane / LPR, piece = lane % LPR;
+    // This lane's 16 columns fill two 16-byte pieces of a 128-byte row; lanes
+    // of the second column block store theirs the other way round, so that
+    // the eight lanes of a row touch eight different bank groups at a time.
+    const int blk = piece >> 2, k0 = (piece & 3) * 2;
+    const uint32_t swap = (D == 128) ? static_cast<uint32_t>(blk) : 0u;
+    const int *table = p.block_table + static_cast<size_t>(seq) * p.max_blocks;
+    // The pages of this warp in tile j (-1 behind the keys).
+    auto pages_of = [&](int j, int (&pid)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int pg = j * kPagesPerTile + 2 * w + u;
+        pid[u] = (j < jhi && pg * kPage < ck.n) ? table[pg] : -1;
+      }
+    };
+    auto load = [&](const uint8_t *pool, const float *scales, int j, const int (&pid)[2], R &raw) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const size_t slice = static_cast<size_t>(max(pid[u], 0)) * p.Hkv + hkv;
+        const int live = pid[u] < 0 ? 0 : min(kPage, ck.n - (j * kPagesPerTile + 2 * w + u) * kPage);
+        raw.scale[u] = live > 0 ? scales[slice] : 0.f;
+        const uint8_t *src = pool + slice * (kPage * D) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < R::PASSES; ++i)
+          raw.w[u][i] = i * R::RPP + row < live ? __ldg(reinterpret_cast<const uint4 *>(src + i * 512))
+                                                : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // One lane's 16 codes as two 16-byte pieces, to row r of the tile at dst.
+    auto put = [&](uint8_t *dst, int r, const uint4 &a, const uint4 &b) {
+      uint8_t *line = dst + blk * CHUNK_BYTES + r * 128;
+      const uint32_t x = r & 7;
+      *reinterpret_cast<uint4 *>(line + ((((k0 + swap) ^ x)) << 4)) = swap ? b : a;
+      *reinterpret_cast<uint4 *>(line + ((((k0 + 1 - swap) ^ x)) << 4)) = swap ? a : b;
+    };
+    R kraw, vraw;
+    int pid[2], pid_next[2];
+    pages_of(jlo, pid);
+    load(p.k_pages, p.k_scales, jlo, pid, kraw);
+    load(p.v_pages, p.v_scales, jlo, pid, vraw);
+    pages_of(jlo + 1, pid_next);
+    bool ok = true;
+    for (int rj = 0; ok && rj < jhi - jlo; ++rj) {
+      const int j = jlo + rj;
+      {
+        const int i = 2 * rj, slot = i % C::NST;
+        if (i >= C::NST) ok = mbar_wait(&sh->empty[slot], (i / C::NST - 1) & 1, abort_flag, p.status);
+#ifdef EXATTN_TEST_WITHHOLD
+        // Test build only: stop before ring index EXATTN_TEST_WITHHOLD, so that
+        // the consumers' waits run out.
+        if (i == EXATTN_TEST_WITHHOLD) break;
+#endif
+        if (!ok) break;
+        uint8_t *dst = sRing + slot * C::TILE_BYTES;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int q = 0; q < R::PASSES; ++q) {
+            const uint4 c = kraw.w[u][q];
+            uint4 a, b;
+            widen4<FMT>(c.x, a.x, a.y);
+            widen4<FMT>(c.y, a.z, a.w);
+            widen4<FMT>(c.z, b.x, b.y);
+            widen4<FMT>(c.w, b.z, b.w);
+            put(dst, (2 * w + u) * kPage + q * R::RPP + row, a, b);
+          }
+        // Read by the softmax warps once S(j) is there.  The ring is deep
+        // enough: K(j + 4) waits for S(j + 2), whose MMAs follow P(j + 1).
+        if (lane < 2) sh->k_scale[rj % kScaleRing][2 * w + lane] = lane ? kraw.scale[1] : kraw.scale[0];
+        fence_async_shared();
+        mbar_arrive(&sh->full[slot]);
+        load(p.k_pages, p.k_scales, j + 1, pid_next, kraw);
+      }
+      {
+        const int i = 2 * rj + 1, slot = i % C::NST;
+        if (i >= C::NST) ok = mbar_wait(&sh->empty[slot], (i / C::NST - 1) & 1, abort_flag, p.status);
+        if (!ok) break;
+        uint8_t *dst = sRing + slot * C::TILE_BYTES;
+        // Tiles that some row sees only in part: their slot in v_bad, or -1.
+        const int edge = j >= edge_hi ? min(j - edge_hi, kEdge - 1)
+                                      : (p.window > 0 && j - edge_0 < kEdge ? kEdge + j - edge_0 : -1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float s = scalbnf(vraw.scale[u], -v_exp);
+          const __half hi = __float2half_rn(s);
+          const __half lo = __float2half_rn(s - __half2float(hi));
+          const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+#pragma unroll
+          for (int q = 0; q < R::PASSES; ++q) {
+            const uint4 c = vraw.w[u][q];
+            uint32_t f[8];
+            widen4<FMT>(c.x, f[0], f[1]);
+            widen4<FMT>(c.y, f[2], f[3]);
+            widen4<FMT>(c.z, f[4], f[5]);
+            widen4<FMT>(c.w, f[6], f[7]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const __half2 x = as_h2(f[e]);
+              f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
+            }
+            const int r = (2 * w + u) * kPage + q * R::RPP + row;
+            if (edge >= 0) {
+              bool bad = false;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if ((f[e] & 0x7c00u) == 0x7c00u) { f[e] &= 0xffff0000u; bad = true; }
+                if ((f[e] & 0x7c000000u) == 0x7c000000u) { f[e] &= 0xffffu; bad = true; }
+              }
+              if (bad) {
+                atomicOr(&sh->v_bad[edge][r >> 5], 1u << (r & 31));
+                sh->any_bad = 1;
+              }
+            }
+            put(dst, r, make_uint4(f[0], f[1], f[2], f[3]), make_uint4(f[4], f[5], f[6], f[7]));
+          }
+        }
+        fence_async_shared();
+        mbar_arrive(&sh->full[slot]);
+        load(p.v_pages, p.v_scales, j + 1, pid_next, vraw);
+      }
+      pages_of(j + 2, pid_next);
+    }
+  } else {
+    // ====================================================== softmax / epilogue
+    regs_inc<kRegsSoft>();
+    const int t = (warp - 8) >> 2;   // row tile of this warpgroup
+    const int quarter = warp & 3;    // TMEM lane quarter this warp may access
+    const int r = quarter * 32 + lane;
+    const int tl = r / p.heads;      // token of the tile; rows behind tokens * heads are idle
+    const int tok = tok0 + t * p.tokens + tl;
+    const int hq = h0 + r - tl * p.heads;
+    const bool valid = tl < p.tokens && tok < ck.nq;
+    const int jst = t == 0 ? js0 : js1, jen = t == 0 ? je0 : je1;
+    const int nt = jen - jst;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + t * 128;
+    const uint32_t o_addr = tmem + lane_off + 256 + t * 128;
+    const size_t out_row = static_cast<size_t>(ck.q0 + (valid ? tok : 0)) * p.Hq + hq;
+    float c_row = p.scale_log2;  // from a raw score to log2 units, but for the page's K scale
+    if (nt > 0) {
+      // This row of Q to f16, its largest element in [2^14, 2^15).
+      uint4 u[D / 8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        u[i] = valid ? __ldg(reinterpret_cast<const uint4 *>(p.q + out_row * D) + i) : make_uint4(0, 0, 0, 0);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
+                                     __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu)));
+      }
+      top = max(top & 0xffffu, top >> 16);
+      int ex = 0;
+      if (top > 0 && top < 0x7f80u) ex = min(100, max(-113, 14 - (static_cast<int>(top >> 7) - 127)));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+      c_row *= __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+      uint8_t *line = smem + t * C::TILE_BYTES + r * 128;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t in[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          f[e] = pack_f16x2(__uint_as_float(in[e] << 16) * up, __uint_as_float(in[e] & 0xffff0000u) * up);
+        *reinterpret_cast<uint4 *>(line + (i >> 3) * CHUNK_BYTES + (((i & 7) ^ (r & 7)) << 4)) =
+            make_uint4(f[0], f[1], f[2], f[3]);
+      }
+      fence_async_shared();
+      mbar_arrive(&sh->q_full[t]);
+    }
+    const float slope2 = kAlibi && valid ? p.slopes[hq] * 1.4426950408889634f : 0.f;
+    float m = -INFINITY;  // reference max, in log2 units of scaled scores
+    float l = 0.f;
+    bool ok = true;
+    for (int jj = 0; jj < nt; ++jj) {
+      const int j = jst + jj;
+      // Visible columns [lo, hi) of this row.  (A row without a token takes one
+      // that forces no masking on a warp whose real rows need none.)
+      const int hi = min(min(BN, ck.n - j * BN), ck.ctx + tok - j * BN + 1);
+      const int lo = p.window > 0 ? ck.ctx + min(tok, ck.nq - 1) - p.window + 1 - j * BN : 0;
+      const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= BN);
+      const bool attempt = !kAlibi && !masked && jj > 0 && __all_sync(0xffffffffu, m != -INFINITY);
+      ok = mbar_wait(&sh->s_full[t], jj & 1, abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[128];
+      load_row(s_addr, sv);
+      float cp[kPagesPerTile];
+      {
+        const float4 *ks = reinterpret_cast<const float4 *>(sh->k_scale[(j - jlo) % kScaleRing]);
+        const float4 a = ks[0], b = ks[1];
+        cp[0] = a.x * c_row; cp[1] = a.y * c_row; cp[2] = a.z * c_row; cp[3] = a.w * c_row;
+        cp[4] = b.x * c_row; cp[5] = b.y * c_row; cp[6] = b.z * c_row; cp[7] = b.w * c_row;
+      }
+      row_loaded(sv);
+      // An unmasked tile first takes P against the running reference as it
+      // stands, without looking for its own max.  Where every row's P sums to
+      // at most 255, each term is below 2^8 and the max-first step below would
+      // have kept the reference too.  Otherwise the S row, which the attempt
+      // left untouched in TMEM, is read again and the tile goes max first.
+      bool fast = false, missed = false;
+      if (attempt) {
+        uint32_t pk[64];
+        float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc)
+          exp_chunk(sv, cc, cp[2 * cc], cp[2 * cc + 1], m, pk + cc * 16, sum_a, sum_b);
+        const float l_tile = (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
+        missed = !(l_tile <= 255.0f);
+        fast = !__any_sync(0xffffffffu, missed);
+        if (fast) {
+          l += l_tile;
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc)
+            tmem_st16(s_addr + cc * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + cc * 16));
+          // The scores are dead on this path: no copy need stay across it.
+#pragma unroll
+          for (int i = 0; i < 128; ++i) asm("" : "=r"(sv[i]));
+        } else {
+          load_row(s_addr, sv);
+          row_loaded(sv);
+        }
+      }
+      if (!fast) {
+        // To scaled scores (log2 units) with the bias; masked ones to -inf,
+        // whatever they were.
+        const float rb = kAlibi ? slope2 * static_cast<float>(j * BN - (ck.ctx + tok)) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          float x = __uint_as_float(sv[i]) * cp[i / kPage];
+          if (kAlibi) x += fmaf(slope2, static_cast<float>(i), rb);
+          sv[i] = __float_as_uint(x);
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i < lo || i >= hi) sv[i] = 0xff800000u;
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 128; i += 8) {
+          m0 = fmax3(m0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+          m1 = fmax3(m1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
+          m2 = fmax3(m2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
+          m3 = fmax3(m3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
+        }
+        const float m_new = fmaxf(m, fmax3(m0, m1, fmaxf(m2, m3)));
+        const bool resc = m_new > m + 8.0f || (missed && m_new > m);
+        const float alpha = resc ? ex2(m - m_new) : 1.0f;
+        if (resc) m = m_new;
+        l *= alpha;
+        // A row that has seen no visible key yet keeps m = -inf; its masked
+        // scores must still give P = 0, not -inf - (-inf).
+        const float m_use = (m == -INFINITY) ? 0.f : m;
+        float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t pk[16];
+          exp_chunk(sv, cc, 1.f, 1.f, m_use, pk, sum_a, sum_b);
+          tmem_st16(s_addr + cc * 16, pk);
+        }
+        l += (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
+        if (jj > 0 && __any_sync(0xffffffffu, resc)) {
+          // Lazy rescale of O.  O is stable here: this tile's S completing
+          // implies the previous PV completed, and this tile's PV waits for
+          // p_full.
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld32(o_addr + cc * 32, ov);
+            tmem_ld_wait(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(o_addr + cc * 32, ov);
+          }
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sh->p_full[t]);
+    }
+    if (ok && nt > 0) {
+      ok = mbar_wait(&sh->o_full[t], (nt - 1) & 1, abort_flag, p.status);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (ok && (nt > 0 || p.nsplit > 1)) {
+      tc_fence_after();
+      // Weight zero for a row that saw no key here (a part of the keys only).
+      const bool seen = l != 0.f;
+      float a = seen ? scalbnf(1.0f / l, v_exp) : 0.f;
+      if (nt > 0 && *reinterpret_cast<volatile int *>(&sh->any_bad)) {
+        // A value that is no number was left out of the edge tiles: rows that
+        // see its key get NaN.
+        for (int e = 0; e < 2 * kEdge; ++e) {
+          const int j = e < kEdge ? edge_hi + e : edge_0 + e - kEdge;
+          if (j < jst || j >= jen || (e >= kEdge && j >= edge_hi)) continue;
+          const int hi = min(BN, ck.ctx + tok - j * BN + 1);
+          const int lo = p.window > 0 ? max(0, ck.ctx + tok - p.window + 1 - j * BN) : 0;
+          for (int i = lo; i < hi; ++i)
+            if (sh->v_bad[e][i >> 5] >> (i & 31) & 1u) a = NAN;
+        }
+      }
+      const float l2 = seen ? m + log2f(l) : -INFINITY;
+      const size_t prow = out_row * p.nsplit + part;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t ov[32];
+        if (nt > 0) {  // (the same for the whole warp)
+          tmem_ld32(o_addr + cc * 32, ov);
+          tmem_ld_wait(ov);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            ov[i] = seen ? __float_as_uint(__uint_as_float(ov[i]) * a) : 0u;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = 0u;
+        }
+        if (valid && p.nsplit == 1) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.o + out_row * D + cc * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              pk[i] = pack_bf16x2(__uint_as_float(ov[8 * q + 2 * i]), __uint_as_float(ov[8 * q + 2 * i + 1]));
+            dst[q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        } else if (valid) {
+          uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + prow * D + cc * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+        }
+      }
+      if (valid) {
+        if (p.nsplit == 1) p.lse[out_row] = l2 * 0.6931471805599453f;
+        else p.l2_part[prow] = l2;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of a split call: one warp per (token, query head), weights
+// 2^(L_part - L).  Block: token of a sequence's chunk (x), eight heads (y).
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefill_q8_join_kernel(const Params p) {
+  grid_dependency_wait();
+  const int s = blockIdx.x / p.max_q, tok = blockIdx.x % p.max_q;
+  const int h = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  Chunk ck;
+  if (h >= p.Hq || !chunk_of(p, s, ck) || tok >= ck.nq) return;
+  const size_t row = static_cast<size_t>(ck.q0 + tok) * p.Hq + h;
+  const float *l2 = p.l2_part + row * p.nsplit;
+  float top = -INFINITY;
+  for (int i = lane; i < p.nsplit; i += 32) top = fmaxf(top, l2[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  constexpr int E = D / 32;  // consecutive elements of this lane
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i = 0; i < p.nsplit; ++i) {
+    const float w = ex2(l2[i] - top);  // NaN where a part failed
+    if (w == 0.f) continue;
+    sum += w;
+    const float *o = p.o_part + (row * p.nsplit + i) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(o + e);
+      acc[e] += w * v.x;
+      acc[e + 1] += w * v.y;
+    }
+  }
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t *>(p.o + row * D + lane * E + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0) p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// How a call is cut: query heads per CTA, tokens per tile, pairs, parts.
+struct Cut {
+  int heads, tokens, pairs, nsplit;
+  long long ctas;
+};
+Cut cut(int S, int Hq, int Hkv, int max_q, int max_blocks) {
+  Cut c;
+  const int G = Hq / Hkv;
+  int n = (G + BM - 1) / BM;  // the fewest equal head groups of at most 128
+  while (G % n) ++n;
+  c.heads = G / n;
+  c.tokens = BM / c.heads;
+  c.pairs = (max_q + 2 * c.tokens - 1) / (2 * c.tokens);
+  const long long base = static_cast<long long>(S) * Hkv * n * c.pairs;
+  // Parts of the keys: as many as fill the SMs, each of two key tiles at least.
+  const int tiles = (max_blocks + kPagesPerTile - 1) / kPagesPerTile;
+  long long ns = base < kSMs ? kSMs / base : 1;
+  if (ns > (tiles + 1) / 2) ns = (tiles + 1) / 2;
+  c.nsplit = ns < 1 ? 1 : static_cast<int>(ns);
+  c.ctas = base * c.nsplit;
+  return c;
+}
+
+template <int D, int FMT, bool kAlibi>
+attn_status_t launch(const Params &p, long long ctas, cudaStream_t stream) {
+  using C = Cfg<D>;
+  // The attribute belongs to the kernel on one device: set once on each.
+  constexpr int kMaxDevices = 64;
+  static std::mutex mutex;
+  static bool set[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ATTN_ERR_CUDA;
+  {
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!set[dev]) {
+      if (cudaFuncSetAttribute(prefill_q8_kernel<D, FMT, kAlibi>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+      set[dev] = true;
+    }
+  }
+  prefill_q8_kernel<D, FMT, kAlibi><<<static_cast<unsigned>(ctas), NUM_THREADS, C::SMEM_BYTES, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (p.nsplit == 1) return ATTN_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.S) * p.max_q, (p.Hq + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, prefill_q8_join_kernel<D>, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q, int d, int max_blocks) {
+  const Cut c = cut(S, Hq, Hkv, max_q, max_blocks);
+  if (c.nsplit == 1) return 0;
+  return static_cast<size_t>(T) * Hq * c.nsplit * (d + 1) * sizeof(float);
+}
+
+attn_status_t launch_prefill_paged_q8(const void *q, const void *k_pages, const void *v_pages,
+                                      const float *k_scales, const float *v_scales, int kv_format,
+                                      const int *block_table, const int *seq_lens, const int *cu_q,
+                                      void *o, float *lse, int S, int Hq, int Hkv, int T, int max_q,
+                                      int d, int max_blocks, int num_pages, float scale, int window,
+                                      const float *slopes, void *workspace, cudaStream_t stream,
+                                      unsigned *status) {
+  const Cut c = cut(S, Hq, Hkv, max_q, max_blocks);
+  if (c.ctas > 0x7fffffffLL || (Hq + kJoinWarps - 1) / kJoinWarps > 65535 ||
+      static_cast<long long>(c.pairs) * (Hq / c.heads) * c.nsplit > 0x7fffffffLL ||
+      (c.nsplit > 1 && static_cast<long long>(S) * max_q > 0x7fffffffLL))
+    return ATTN_ERR_INVALID_ARG;
+  Params p{};
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.k_pages = static_cast<const uint8_t *>(k_pages);
+  p.v_pages = static_cast<const uint8_t *>(v_pages);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.lse = lse;
+  if (c.nsplit > 1) {
+    p.o_part = static_cast<float *>(workspace);
+    p.l2_part = p.o_part + static_cast<size_t>(T) * Hq * c.nsplit * d;
+  }
+  p.slopes = slopes;
+  p.status = status;
+  p.S = S;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.T = T;
+  p.max_q = max_q;
+  p.max_blocks = max_blocks;
+  p.num_pages = num_pages;
+  p.heads = c.heads;
+  p.tokens = c.tokens;
+  p.pairs = c.pairs;
+  p.nsplit = c.nsplit;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.window = window;
+  const bool e4m3 = kv_format == ATTN_KV_E4M3;
+  if (d == 128) {
+    if (slopes) return e4m3 ? launch<128, ATTN_KV_E4M3, true>(p, c.ctas, stream)
+                            : launch<128, ATTN_KV_INT8, true>(p, c.ctas, stream);
+    return e4m3 ? launch<128, ATTN_KV_E4M3, false>(p, c.ctas, stream)
+                : launch<128, ATTN_KV_INT8, false>(p, c.ctas, stream);
+  }
+  if (slopes) return e4m3 ? launch<64, ATTN_KV_E4M3, true>(p, c.ctas, stream)
+                          : launch<64, ATTN_KV_INT8, true>(p, c.ctas, stream);
+  return e4m3 ? launch<64, ATTN_KV_E4M3, false>(p, c.ctas, stream)
+              : launch<64, ATTN_KV_INT8, false>(p, c.ctas, stream);
+}
+
+}  // namespace exattn

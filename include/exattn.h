@@ -88,6 +88,19 @@ typedef enum {
                                    1024-byte aligned and returned at once; the gradients
                                    are undefined */
 
+/* Element type of the calls that take more than one. */
+#define ATTN_DTYPE_BF16 0
+#define ATTN_DTYPE_F32 1
+
+/* Where the rows of a [B, H, N, d] tensor lie: strides in elements between batch
+ * entries, heads and tokens; the d elements of a row are consecutive.  Every
+ * stride is a non-negative multiple of 16 bytes; one that is 0 repeats an input,
+ * and an output has none over an extent above 1, and no two rows in one place.
+ * A token-major [T, H, d] tensor is the case B = 1, N = T. */
+typedef struct {
+    int64_t batch, head, token;
+} attn_strides_t;
+
 /*
  * attn_fwd -- bf16 prefill, forward only.  Lab 01 steps 2 and 4 of the Phase 08
  * page: Q is split into row tiles; for each, the kernel walks the K/V column
@@ -277,6 +290,165 @@ EXATTN_API attn_status_t attn_decode_paged_q8(const void *q, const void *k_pages
                                               int max_blocks, int num_pages, float scale,
                                               void *workspace, size_t workspace_bytes,
                                               attn_stream_t stream);
+
+/*
+ * attn_kv_write_paged_q8 -- write a chunk's new keys and values into the 8-bit
+ * cache that attn_decode_paged_q8 and attn_prefill_paged_q8 read (the KV-cache
+ * quantisation answer of the screna.ai interview page; the pages say that the
+ * cache is kept in 8 bits with group-wise scales, not how it is filled).  The
+ * chunk of sequence s is the last qlen_s = cu_q[s+1] - cu_q[s] of its seq_lens[s]
+ * tokens, as for attn_prefill_paged: qlen_s = 1 is a decode step.  For each
+ * (page, K/V head) slice the chunk touches, of K and of V, with qmax 448 (E4M3)
+ * or 127 (INT8):
+ *   s' = max(s if the page holds earlier tokens of the sequence,
+ *            amax(new tokens) / qmax, 2^-126)
+ *   new codes     = x / s', earlier codes = code * s / s', each rounded to the
+ *                   format's nearest value, ties to even,
+ * and the slice's scale becomes s'.  So a page's scale only grows while it
+ * fills, a page whose first slot is written starts afresh, and the same call
+ * twice leaves what it left the first time.  If the new tokens of a slice hold a
+ * NaN or an infinity (or its earlier scale is none of the finite numbers) its
+ * scale becomes NaN and the new codes 0: attention over it is then NaN.
+ *
+ *   k, v         [T, Hkv, d] bf16: rows cu_q[s] .. cu_q[s+1]-1 are sequence s's
+ *                chunk; strides in elements between tokens and heads (multiples
+ *                of 8), so that both may be slices of one projection's output
+ *   k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, kv_format
+ *                as for attn_decode_paged_q8, the pages and scales (in, out)
+ *   cu_q         [S+1] int32, non-decreasing, cu_q[0] = 0, cu_q[S] <= T
+ *   max_q        an upper bound of every qlen_s (sizes the grid)
+ * Slots and pages that hold none of the chunk's tokens stay as they are, but for
+ * the earlier tokens of a chunk's first page.  A page that is written must be
+ * one sequence's alone; two that write it leave either's bytes.  A sequence
+ * whose lengths are inconsistent (as for attn_prefill_paged) is skipped, and so
+ * is a page id outside [0, num_pages); both set ATTN_DEV_BAD_PAGE in the word of
+ * attn_device_status, and no out-of-range address is dereferenced.  T == 0 or
+ * max_q == 0 is a no-op.  d in {64, 128}; page_size == 16.
+ */
+EXATTN_API attn_status_t attn_kv_write_paged_q8(
+    const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+    int64_t v_token_stride, int64_t v_head_stride, void *k_pages, void *v_pages, float *k_scales,
+    float *v_scales, int kv_format, const int32_t *block_table, const int32_t *seq_lens,
+    const int32_t *cu_q, int S, int Hkv, int T, int max_q, int d, int page_size, int max_blocks,
+    int num_pages, attn_stream_t stream);
+
+/*
+ * attn_kv_read_paged_q8 -- the last qlen_s = cu_q[s+1] - cu_q[s] tokens of each
+ * sequence out of the 8-bit cache (screna.ai interview page: KV-cache
+ * quantisation), as dense tensors: element = scale * code, rounded once to
+ * dtype (ATTN_DTYPE_BF16 or ATTN_DTYPE_F32).
+ *
+ *   k, v         [T, Hkv, d] (out), dense: rows cu_q[s] .. cu_q[s+1]-1
+ *   others       as for attn_kv_write_paged_q8, the pages and scales (in)
+ * Rows of no sequence stay as they are.  A page id outside the pool gives NaN
+ * rows and sets ATTN_DEV_BAD_PAGE; a sequence of inconsistent lengths is skipped
+ * and sets it.  T == 0 or max_q == 0 is a no-op.
+ */
+EXATTN_API attn_status_t attn_kv_read_paged_q8(
+    const void *k_pages, const void *v_pages, const float *k_scales, const float *v_scales,
+    int kv_format, const int32_t *block_table, const int32_t *seq_lens, const int32_t *cu_q,
+    void *k, void *v, int dtype, int S, int Hkv, int T, int max_q, int d, int page_size,
+    int max_blocks, int num_pages, attn_stream_t stream);
+
+/*
+ * attn_prefill_paged_q8 -- attn_prefill_paged over the 8-bit cache (Phase 08
+ * page, Concepts: chunked prefill, paged attention; screna.ai interview page:
+ * KV-cache quantisation).  Queries, chunks, window, ALiBi, outputs, errors and
+ * bad pages as for attn_prefill_paged; pages, scales and kv_format as for
+ * attn_decode_paged_q8 (the chunk's own tokens have been written, e.g. by
+ * attn_kv_write_paged_q8).  Rows of no sequence stay as they are.
+ * A value of V that is no finite number reaches every element of the rows that
+ * see its token, and only those.
+ *
+ *   workspace    device scratch of at least attn_prefill_q8_workspace_bytes(...)
+ *                bytes, owned by the caller; no initialisation needed, NULL
+ *                where that is 0.  Calls that may run at the same time need one
+ *                each.
+ * Inside the kernel queries are rounded to f16 after a per-row power-of-two
+ * normalisation, the V elements (scale * code) and P to f16; scores, sums and
+ * outputs accumulate in float32.
+ */
+EXATTN_API size_t attn_prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q, int d,
+                                                  int max_blocks, int page_size);
+EXATTN_API attn_status_t attn_prefill_paged_q8(
+    const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+    const float *v_scales, int kv_format, const int32_t *block_table, const int32_t *seq_lens,
+    const int32_t *cu_q, void *o, float *lse, int S, int Hq, int Hkv, int T, int max_q, int d,
+    int page_size, int max_blocks, int num_pages, float scale, int window,
+    const float *alibi_slopes, void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * attn_rope -- rotary positions of the queries and keys that the attention calls
+ * take (no counterpart on the pages, which take q and k as they come).  The
+ * first rot elements of each row form rot/2 pairs, (x_i, x_{i+rot/2}), or with
+ * interleaved != 0 (x_2i, x_{2i+1}); at position t pair i turns by the angle
+ * t * inv_freq[i]:
+ *   y = factor * (x cos - x' sin),   y' = factor * (x sin + x' cos),
+ * and the elements from rot on pass as they are.  transpose != 0 applies the
+ * transposed map, y = factor * (x cos + x' sin), y' = factor * (x' cos - x sin):
+ * the gradient of the other.
+ *
+ *   q, q_out     [B, Hq, N, d], k, k_out [B, Hkv, N, d], dtype ATTN_DTYPE_BF16 or
+ *                ATTN_DTYPE_F32, each with strides of its own (NULL: dense); an
+ *                output may be its input (same pointer and strides).  k and k_out
+ *                may be NULL with Hkv == 0.
+ *   positions    int32; batch entry b's N positions start at b *
+ *                position_stride (0: shared by all).  Any value, negative too.
+ *   inv_freq     [rot/2] float64 (device, 8-byte aligned), radians a position
+ *   rot          even, 2 <= rot <= d;  d in {64, 128};  factor finite
+ * Angles are reduced in 64 bits; rotations are float32, rounded once.  N == 0 or
+ * B == 0 is a no-op.
+ */
+EXATTN_API attn_status_t attn_rope(
+    const void *q, const attn_strides_t *q_strides, void *q_out,
+    const attn_strides_t *q_out_strides, const void *k, const attn_strides_t *k_strides,
+    void *k_out, const attn_strides_t *k_out_strides, const int32_t *positions,
+    int64_t position_stride, const double *inv_freq, int dtype, int B, int Hq, int Hkv, int N,
+    int d, int rot, int interleaved, float factor, int transpose, attn_stream_t stream);
+
+/*
+ * attn_norm_rope -- attn_rope (not transposed) of the rows after an RMS norm of
+ * each head (no counterpart on the pages):
+ *   z = q_weight * x * (mean(x^2) + eps)^(-1/2),  then the rotation of z,
+ * with k_weight for the keys.  Weights: [d] of dtype, shared by the heads; eps
+ * finite and > 0.  Other arguments as for attn_rope.
+ */
+EXATTN_API attn_status_t attn_norm_rope(
+    const void *q, const attn_strides_t *q_strides, const void *q_weight, void *q_out,
+    const attn_strides_t *q_out_strides, const void *k, const attn_strides_t *k_strides,
+    const void *k_weight, void *k_out, const attn_strides_t *k_out_strides,
+    const int32_t *positions, int64_t position_stride, const double *inv_freq, int dtype, int B,
+    int Hq, int Hkv, int N, int d, int rot, int interleaved, float factor, float eps,
+    attn_stream_t stream);
+
+/*
+ * attn_norm_rope_bwd -- gradients of attn_norm_rope (no counterpart on the
+ * pages).  With u the transposed rotation of dy, xhat = x * r, r = (mean(x^2) +
+ * eps)^(-1/2) and w the side's weights:
+ *   dw = sum over batch, heads and tokens of u * xhat,
+ *   dx = r * (w * u - xhat * mean(w * u * xhat)).
+ *
+ *   q, k         the inputs of attn_norm_rope; dq_out, dk_out the gradients of
+ *                its outputs; dq, dk (out): all of dtype, with strides of their
+ *                own.  dq may be dq_out or q, dk likewise (same pointer and
+ *                strides).
+ *   dq_weight, dk_weight   [d] float32 (out)
+ *   workspace    device scratch of at least attn_norm_rope_bwd_workspace_bytes(B,
+ *                Hq, Hkv, N, d) bytes, owned by the caller; no initialisation
+ *                needed
+ * The result is deterministic: no atomics.  With B == 0 or N == 0 the weights'
+ * gradients are 0.
+ */
+EXATTN_API size_t attn_norm_rope_bwd_workspace_bytes(int B, int Hq, int Hkv, int N, int d);
+EXATTN_API attn_status_t attn_norm_rope_bwd(
+    const void *q, const attn_strides_t *q_strides, const void *q_weight, const void *dq_out,
+    const attn_strides_t *dq_out_strides, void *dq, const attn_strides_t *dq_strides,
+    float *dq_weight, const void *k, const attn_strides_t *k_strides, const void *k_weight,
+    const void *dk_out, const attn_strides_t *dk_out_strides, void *dk,
+    const attn_strides_t *dk_strides, float *dk_weight, const int32_t *positions,
+    int64_t position_stride, const double *inv_freq, int dtype, int B, int Hq, int Hkv, int N,
+    int d, int rot, int interleaved, float factor, float eps, void *workspace,
+    size_t workspace_bytes, attn_stream_t stream);
 
 /*
  * attn_decode_paged_noalloc -- attn_decode_paged for callers that cannot
