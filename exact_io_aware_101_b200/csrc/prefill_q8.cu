@@ -17,10 +17,11 @@
 //    group, and a chunk of a few tokens fills a tile instead of G of them.
 //  * 16 warps in four warpgroups:
 //      warp 0       allocates TMEM and issues every tcgen05.mma;
-//      warps 4-7    widen: each takes two pages of a 128-key tile, reads their
-//                   codes with 16-byte loads one tile ahead of their use,
-//                   converts them and stores them into a ring of NST slots in
-//                   the 128-byte-swizzled layout that the MMAs read;
+//      warp 1       brings the codes of each 128-key tile to shared memory, one
+//                   untiled bulk copy per page (its slice is contiguous);
+//      warps 4-7    widen: each takes two pages of a tile, converts their codes
+//                   and stores them into a ring of NST slots in the
+//                   128-byte-swizzled layout that the MMAs read;
 //      warps 8-11   softmax, correction and epilogue of tile 0, warps 12-15 of
 //                   tile 1; before that they bring the tiles' queries to f16.
 //    Measured on the chunked workload (16 chunks of 512, Hq = 32, Hkv = 8, d =
@@ -59,21 +60,24 @@ constexpr int BN = 128;  // keys of a tile
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = BN / kPage;
 constexpr int NUM_THREADS = 512;
-constexpr int kRegsMma = 48, kRegsWiden = 112, kRegsSoft = 176;
+constexpr int kRegsMma = 64, kRegsWiden = 80, kRegsSoft = 184;
 static_assert(128 * (kRegsMma + kRegsWiden + 2 * kRegsSoft) <= NUM_THREADS * 128,
               "setmaxnreg split must fit the block's launch registers");
 constexpr int kRankMax = NUM_THREADS;   // sequences ranked by length
 constexpr int CHUNK_BYTES = 128 * 128;  // one 128-row x 128-byte swizzle column block
 constexpr int kSMs = 148;
-constexpr int kScaleRing = 8;  // tiles whose K scales are kept (four would do, see issue order)
+constexpr int kScaleRing = 8;  // tiles whose page scales are kept in shared memory
 constexpr int kEdge = 4;       // tiles that a row may see in part, at either end of the walk
 
 template <int D>
 struct Cfg {
   static constexpr int TILE_BYTES = BM * D * 2;  // a Q, K or V tile in f16
   static constexpr int NST = (D == 64) ? 8 : 4;  // ring slots
+  static constexpr int RAW_BYTES = BN * D;       // a K or V tile in codes
+  static constexpr int NRAW = (D == 64) ? 4 : 2; // raw slots: K and V in turn
   static constexpr int RING_OFF = 2 * TILE_BYTES;
-  static constexpr int BAR_OFF = RING_OFF + NST * TILE_BYTES;
+  static constexpr int RAW_OFF = RING_OFF + NST * TILE_BYTES;
+  static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW_BYTES;
   static constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;  // + 1 KB align slack
   static constexpr uint32_t IDESC_QK =  // as idesc_bf16_f32, with both operand formats 0 (f16)
       idesc_bf16_f32(BM, BN, false, false) & ~((7u << 7) | (7u << 10));
@@ -82,6 +86,8 @@ struct Cfg {
 };
 
 struct Shared {
+  uint64_t raw_full[4];
+  uint64_t raw_empty[4];
   uint64_t full[8];
   uint64_t empty[8];
   uint64_t q_full[2];
@@ -90,6 +96,7 @@ struct Shared {
   uint64_t o_full[2];
   uint64_t mma_done;
   alignas(16) float k_scale[kScaleRing][kPagesPerTile];
+  alignas(16) float v_scale[kScaleRing][kPagesPerTile];
   unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with a NaN or infinite value
   unsigned v_top;                      // largest finite |V scale| of the CTA's pages, as bits
   int any_bad;
@@ -198,15 +205,6 @@ __device__ __forceinline__ bool chunk_of(const Params &p, int s, Chunk &c) {
          c.n <= static_cast<long long>(p.max_blocks) * kPage;
 }
 
-// A tile's raw codes in flight: each widening warp's two pages, 16 bytes a lane.
-template <int D>
-struct Raw {
-  static constexpr int RPP = 512 / D;          // rows per 512-byte pass
-  static constexpr int PASSES = kPage / RPP;   // passes per page
-  uint4 w[2][PASSES];
-  float scale[2];
-};
-
 template <int D, int FMT, bool kAlibi>
 __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params p) {
   using C = Cfg<D>;
@@ -231,8 +229,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
   const int group = (rem % per_pair) / p.nsplit, part = rem % p.nsplit;
   int seq = rank_of;
   if (p.S > 1 && p.S <= kRankMax) {
-    __shared__ int s_len[kRankMax];
-    __shared__ int s_seq;
+    int *s_len = reinterpret_cast<int *>(smem);  // (where the queries come later)
+    int &s_seq = s_len[kRankMax];
     const int t = static_cast<int>(threadIdx.x);
     if (t < p.S) s_len[t] = p.seq_lens[t];
     __syncthreads();
@@ -244,6 +242,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     }
     __syncthreads();
     seq = s_seq;
+    __syncthreads();
   }
   Chunk ck;
   if (!chunk_of(p, seq, ck)) {
@@ -278,6 +277,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
 
   // ---- every page of those tiles must be in the pool; and their largest V scale.
   if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NRAW; ++i) {
+      mbar_init(&sh->raw_full[i], 1);
+      mbar_init(&sh->raw_empty[i], 128);
+    }
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&sh->full[i], 128);
       mbar_init(&sh->empty[i], 1);
@@ -412,134 +415,167 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       // Every MMA issued above must finish before TMEM is released.
       tc_commit(&sh->mma_done);
       mbar_wait_drain(&sh->mma_done, 0, p.status);
+    } else if (warp == 1) {
+      // =============================================================== copies
+      // Lane u < 8 brings page u of a tile: its K, then its V slice, one untiled
+      // copy each, and its scales, which it reads a tile ahead.  Slots behind
+      // the keys keep what they held: their scores are masked, and the widening
+      // of such a tile lets no value that is no number pass.
+      const int *table = p.block_table + static_cast<size_t>(seq) * p.max_blocks;
+      const int u = lane & 7;
+      auto slice_of = [&](int j) {
+        const int pg = j * kPagesPerTile + u;
+        return j < jhi && pg * kPage < ck.n ? static_cast<long long>(table[pg]) * p.Hkv + hkv : -1LL;
+      };
+      const float v_unit = __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23);
+      int issued = 0;
+      long long slice = slice_of(jlo);
+      float ks = slice >= 0 ? p.k_scales[slice] : 0.f, vs = slice >= 0 ? p.v_scales[slice] : 0.f;
+      bool go = true;
+      for (int j = jlo; go && j < jhi; ++j) {
+        const long long next = slice_of(j + 1);
+        const unsigned pages = __popc(__ballot_sync(0xffffffffu, slice >= 0) & 0xffu);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int i = 2 * (j - jlo) + kv, slot = i % C::NRAW;
+          if (lane == 0 && i >= C::NRAW)
+            go = mbar_wait(&sh->raw_empty[slot], (i / C::NRAW - 1) & 1, abort_flag, p.status);
+          go = __shfl_sync(0xffffffffu, go, 0);
+#ifdef EXATTN_TEST_WITHHOLD
+          // Test build only: stop before ring index EXATTN_TEST_WITHHOLD, so that
+          // the consumers' waits run out.
+          if (i == EXATTN_TEST_WITHHOLD) go = false;
+#endif
+          if (!go) break;
+          // (The softmax has read the K scales of eight tiles before: S of four
+          // tiles before this one was needed for its ring slot.)
+          if (lane < 8) {
+            if (kv == 0) sh->k_scale[(j - jlo) % kScaleRing][u] = ks;
+            else sh->v_scale[(j - jlo) % kScaleRing][u] = vs * v_unit;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&sh->raw_full[slot], pages * (kPage * D));
+          __syncwarp();
+          if (lane < 8 && slice >= 0)
+            bulk_load(smem + C::RAW_OFF + slot * C::RAW_BYTES + u * (kPage * D),
+                      (kv ? p.v_pages : p.k_pages) + static_cast<size_t>(slice) * (kPage * D), kPage * D,
+                      &sh->raw_full[slot]);
+          issued = i + 1;
+        }
+        slice = next;
+        ks = slice >= 0 ? p.k_scales[slice] : 0.f;
+        vs = slice >= 0 ? p.v_scales[slice] : 0.f;
+      }
+      // No copy may still be writing shared memory when the CTA exits.
+      if (lane == 0)
+        for (int i = max(0, issued - C::NRAW); i < issued; ++i)
+          mbar_wait_drain(&sh->raw_full[i % C::NRAW], (i / C::NRAW) & 1, p.status);
     }
   } else if (warp < 8) {
     // =============================================================== widening
     regs_dec<kRegsWiden>();
-    using R = Raw<D>;
     const int w = warp - 4;
-    constexpr int LPR = D / 16;  // lanes per row
-    const int row = lane / LPR, piece = lane % LPR;
-    // This lane's 16 columns fill two 16-byte pieces of a 128-byte row; lanes
-    // of the second column block store theirs the other way round, so that
-    // the eight lanes of a row touch eight different bank groups at a time.
+    constexpr int LPR = D / 16;         // lanes per row
+    constexpr int RPP = 32 / LPR;       // rows per 512-byte pass
+    constexpr int PASSES = kPage / RPP; // passes per page
+    // A lane takes 16 columns: two 16-byte pieces of a 128-byte row of f16.  The
+    // second column block (d = 128) lies a multiple of all banks behind the
+    // first, so its lanes take the other row of each pair: the swizzle then
+    // sends the eight lanes of a store to eight different bank groups.
+    const int piece = lane % LPR;
     const int blk = piece >> 2, k0 = (piece & 3) * 2;
-    const uint32_t swap = (D == 128) ? static_cast<uint32_t>(blk) : 0u;
-    const int *table = p.block_table + static_cast<size_t>(seq) * p.max_blocks;
-    // The pages of this warp in tile j (-1 behind the keys).
-    auto pages_of = [&](int j, int (&pid)[2]) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int pg = j * kPagesPerTile + 2 * w + u;
-        pid[u] = (j < jhi && pg * kPage < ck.n) ? table[pg] : -1;
-      }
-    };
-    auto load = [&](const uint8_t *pool, const float *scales, int j, const int (&pid)[2], R &raw) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const size_t slice = static_cast<size_t>(max(pid[u], 0)) * p.Hkv + hkv;
-        const int live = pid[u] < 0 ? 0 : min(kPage, ck.n - (j * kPagesPerTile + 2 * w + u) * kPage);
-        raw.scale[u] = live > 0 ? scales[slice] : 0.f;
-        const uint8_t *src = pool + slice * (kPage * D) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < R::PASSES; ++i)
-          raw.w[u][i] = i * R::RPP + row < live ? __ldg(reinterpret_cast<const uint4 *>(src + i * 512))
-                                                : make_uint4(0, 0, 0, 0);
-      }
-    };
+    const int row = (lane / LPR) ^ blk;
+    const int from = w * (2 * kPage * D) + row * D + piece * 16;  // in a raw tile
     // One lane's 16 codes as two 16-byte pieces, to row r of the tile at dst.
     auto put = [&](uint8_t *dst, int r, const uint4 &a, const uint4 &b) {
       uint8_t *line = dst + blk * CHUNK_BYTES + r * 128;
-      const uint32_t x = r & 7;
-      *reinterpret_cast<uint4 *>(line + ((((k0 + swap) ^ x)) << 4)) = swap ? b : a;
-      *reinterpret_cast<uint4 *>(line + ((((k0 + 1 - swap) ^ x)) << 4)) = swap ? a : b;
+      const int x = r & 7;
+      *reinterpret_cast<uint4 *>(line + ((k0 ^ x) << 4)) = a;
+      *reinterpret_cast<uint4 *>(line + (((k0 + 1) ^ x) << 4)) = b;
     };
-    R kraw, vraw;
-    int pid[2], pid_next[2];
-    pages_of(jlo, pid);
-    load(p.k_pages, p.k_scales, jlo, pid, kraw);
-    load(p.v_pages, p.v_scales, jlo, pid, vraw);
-    pages_of(jlo + 1, pid_next);
-    bool ok = true;
-    for (int rj = 0; ok && rj < jhi - jlo; ++rj) {
+    // Raw entry i is in its slot, and the ring's slot for it is free.
+    auto ready = [&](int i) {
+      if (!mbar_wait(&sh->raw_full[i % C::NRAW], (i / C::NRAW) & 1, abort_flag, p.status)) return false;
+      return i < C::NST || mbar_wait(&sh->empty[i % C::NST], (i / C::NST - 1) & 1, abort_flag, p.status);
+    };
+    auto done = [&](int i) {
+      fence_async_shared();
+      mbar_arrive(&sh->full[i % C::NST]);
+      mbar_arrive(&sh->raw_empty[i % C::NRAW]);
+    };
+    for (int rj = 0; rj < jhi - jlo; ++rj) {
       const int j = jlo + rj;
       {
-        const int i = 2 * rj, slot = i % C::NST;
-        if (i >= C::NST) ok = mbar_wait(&sh->empty[slot], (i / C::NST - 1) & 1, abort_flag, p.status);
-#ifdef EXATTN_TEST_WITHHOLD
-        // Test build only: stop before ring index EXATTN_TEST_WITHHOLD, so that
-        // the consumers' waits run out.
-        if (i == EXATTN_TEST_WITHHOLD) break;
-#endif
-        if (!ok) break;
-        uint8_t *dst = sRing + slot * C::TILE_BYTES;
+        const int i = 2 * rj;
+        if (!ready(i)) break;
+        const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
+        uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int q = 0; q < R::PASSES; ++q) {
-            const uint4 c = kraw.w[u][q];
-            uint4 a, b;
-            widen4<FMT>(c.x, a.x, a.y);
-            widen4<FMT>(c.y, a.z, a.w);
-            widen4<FMT>(c.z, b.x, b.y);
-            widen4<FMT>(c.w, b.z, b.w);
-            put(dst, (2 * w + u) * kPage + q * R::RPP + row, a, b);
-          }
-        // Read by the softmax warps once S(j) is there.  The ring is deep
-        // enough: K(j + 4) waits for S(j + 2), whose MMAs follow P(j + 1).
-        if (lane < 2) sh->k_scale[rj % kScaleRing][2 * w + lane] = lane ? kraw.scale[1] : kraw.scale[0];
-        fence_async_shared();
-        mbar_arrive(&sh->full[slot]);
-        load(p.k_pages, p.k_scales, j + 1, pid_next, kraw);
+        for (int u = 0; u < 2 * PASSES; ++u) {
+          const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
+          uint4 a, b;
+          widen4<FMT>(c.x, a.x, a.y);
+          widen4<FMT>(c.y, a.z, a.w);
+          widen4<FMT>(c.z, b.x, b.y);
+          widen4<FMT>(c.w, b.z, b.w);
+          put(dst, 2 * w * kPage + u * RPP + row, a, b);
+        }
+        done(i);
       }
       {
-        const int i = 2 * rj + 1, slot = i % C::NST;
-        if (i >= C::NST) ok = mbar_wait(&sh->empty[slot], (i / C::NST - 1) & 1, abort_flag, p.status);
-        if (!ok) break;
-        uint8_t *dst = sRing + slot * C::TILE_BYTES;
+        const int i = 2 * rj + 1;
+        if (!ready(i)) break;
+        const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
+        uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
+        const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[rj % kScaleRing][2 * w]);
         // Tiles that some row sees only in part: their slot in v_bad, or -1.
         const int edge = j >= edge_hi ? min(j - edge_hi, kEdge - 1)
                                       : (p.window > 0 && j - edge_0 < kEdge ? kEdge + j - edge_0 : -1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float s = scalbnf(vraw.scale[u], -v_exp);
+        for (int u = 0; u < 2 * PASSES; ++u) {
+          const float s = u < PASSES ? vs.x : vs.y;
           const __half hi = __float2half_rn(s);
           const __half lo = __float2half_rn(s - __half2float(hi));
           const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+          const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
+          uint32_t f[8];
+          widen4<FMT>(c.x, f[0], f[1]);
+          widen4<FMT>(c.y, f[2], f[3]);
+          widen4<FMT>(c.z, f[4], f[5]);
+          widen4<FMT>(c.w, f[6], f[7]);
 #pragma unroll
-          for (int q = 0; q < R::PASSES; ++q) {
-            const uint4 c = vraw.w[u][q];
-            uint32_t f[8];
-            widen4<FMT>(c.x, f[0], f[1]);
-            widen4<FMT>(c.y, f[2], f[3]);
-            widen4<FMT>(c.z, f[4], f[5]);
-            widen4<FMT>(c.w, f[6], f[7]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __half2 x = as_h2(f[e]);
-              f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
-            }
-            const int r = (2 * w + u) * kPage + q * R::RPP + row;
-            if (edge >= 0) {
+          for (int e = 0; e < 8; ++e) {
+            const __half2 x = as_h2(f[e]);
+            f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
+          }
+          put(dst, 2 * w * kPage + u * RPP + row, make_uint4(f[0], f[1], f[2], f[3]),
+              make_uint4(f[4], f[5], f[6], f[7]));
+        }
+        if (edge >= 0) {
+          // What this lane stored, again: values that are no numbers leave.
+#pragma unroll 1
+          for (int u = 0; u < 2 * PASSES; ++u) {
+            const int r = 2 * w * kPage + u * RPP + row;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              uint32_t *at = reinterpret_cast<uint32_t *>(dst + blk * CHUNK_BYTES + r * 128 + (((k0 + h) ^ (r & 7)) << 4));
               bool bad = false;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if ((f[e] & 0x7c00u) == 0x7c00u) { f[e] &= 0xffff0000u; bad = true; }
-                if ((f[e] & 0x7c000000u) == 0x7c000000u) { f[e] &= 0xffffu; bad = true; }
+              for (int e = 0; e < 4; ++e) {
+                uint32_t f = at[e];
+                if ((f & 0x7c00u) == 0x7c00u) { f &= 0xffff0000u; bad = true; }
+                if ((f & 0x7c000000u) == 0x7c000000u) { f &= 0xffffu; bad = true; }
+                if (bad) at[e] = f;
               }
               if (bad) {
                 atomicOr(&sh->v_bad[edge][r >> 5], 1u << (r & 31));
                 sh->any_bad = 1;
               }
             }
-            put(dst, r, make_uint4(f[0], f[1], f[2], f[3]), make_uint4(f[4], f[5], f[6], f[7]));
           }
         }
-        fence_async_shared();
-        mbar_arrive(&sh->full[slot]);
-        load(p.v_pages, p.v_scales, j + 1, pid_next, vraw);
+        done(i);
       }
-      pages_of(j + 2, pid_next);
     }
   } else {
     // ====================================================== softmax / epilogue
