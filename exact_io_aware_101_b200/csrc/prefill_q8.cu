@@ -60,7 +60,7 @@ constexpr int BN = 128;  // keys of a tile
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = BN / kPage;
 constexpr int NUM_THREADS = 512;
-constexpr int kRegsMma = 64, kRegsWiden = 80, kRegsSoft = 184;
+constexpr int kRegsMma = 72, kRegsWiden = 72, kRegsSoft = 184;
 static_assert(128 * (kRegsMma + kRegsWiden + 2 * kRegsSoft) <= NUM_THREADS * 128,
               "setmaxnreg split must fit the block's launch registers");
 constexpr int kRankMax = NUM_THREADS;   // sequences ranked by length
@@ -136,6 +136,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred one;\n\t"
+      "elect.sync _|one, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, one;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // Shared-memory stores of this thread become visible to the tensor core's reads.
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -350,7 +360,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
   if (warp < 4) {
     // ================================================================== MMA
     regs_dec<kRegsMma>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
+      // The whole warp walks the schedule and one elected lane issues: with the
+      // control flow uniform, the descriptors stay in uniform registers.  (One
+      // lane alone took 110-160 cycles an MMA, more than the 64 it runs for: 680
+      // us for the 16 chunks of 512, against 586 this way.)
+      const bool one = elect_one();
       const uint32_t ring_base = smem_u32(sRing);
       auto slot_of = [](int i) { return i % C::NST; };
       auto wait_full = [&](int i) {
@@ -365,17 +380,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * CHUNK_BYTES + (ks & 3) * 32) >> 4;
-          mma_ss(tmem + t * 128, qd + off, kd + off, C::IDESC_QK, ks > 0);
+          if (one) mma_ss(tmem + t * 128, qd + off, kd + off, C::IDESC_QK, ks > 0);
         }
-        tc_commit(&sh->s_full[t]);
+        if (one) tc_commit(&sh->s_full[t]);
       };
       auto issue_pv = [&](int t, int vidx, bool acc) {  // O_t (+)= P_t V
         const uint64_t vd = vdesc0 + ((slot_of(vidx) * C::TILE_BYTES) >> 4);
 #pragma unroll
         for (int ks = 0; ks < BN / 16; ++ks)
-          mma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4),
-                 C::IDESC_PV, (acc || ks > 0) ? 1u : 0u);
-        tc_commit(&sh->o_full[t]);
+          if (one)
+            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4),
+                   C::IDESC_PV, (acc || ks > 0) ? 1u : 0u);
+        if (one) tc_commit(&sh->o_full[t]);
       };
       // Tile j sits at ring index 2 * (j - jlo) (K) and one behind (V).
       auto has = [&](int t, int j) {
@@ -388,7 +404,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         tc_fence_after();
         if (has(0, jlo)) issue_s(0, 0);
         if (has(1, jlo)) issue_s(1, 0);
-        tc_commit(&sh->empty[slot_of(0)]);
+        if (one) tc_commit(&sh->empty[slot_of(0)]);
       }
       for (int rj = 0; ok && rj < jhi - jlo; ++rj) {
         const int j = jlo + rj;
@@ -408,12 +424,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           tc_fence_after();
           issue_pv(1, 2 * rj + 1, j > js1);
         }
-        tc_commit(&sh->empty[slot_of(2 * rj + 1)]);
+        if (one) tc_commit(&sh->empty[slot_of(2 * rj + 1)]);
         if (more && has(1, j + 1)) issue_s(1, 2 * rj + 2);
-        if (more) tc_commit(&sh->empty[slot_of(2 * rj + 2)]);
+        if (more && one) tc_commit(&sh->empty[slot_of(2 * rj + 2)]);
       }
       // Every MMA issued above must finish before TMEM is released.
-      tc_commit(&sh->mma_done);
+      if (one) tc_commit(&sh->mma_done);
       mbar_wait_drain(&sh->mma_done, 0, p.status);
     } else if (warp == 1) {
       // =============================================================== copies
