@@ -71,11 +71,6 @@ _STATUS = {0: "ATTN_OK", 1: "ATTN_ERR_INVALID_ARG", 2: "ATTN_ERR_UNSUPPORTED", 3
 _lib = None
 
 
-class _Strides(ctypes.Structure):
-    """attn_strides_t: elements between batch entries, heads and tokens."""
-    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
-
-
 class AttnError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__("%s failed: %s" % (what, _STATUS.get(code, "status %d" % code)))
@@ -128,7 +123,7 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.attn_decode_paged_q8.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, vp, vp, ci, ci, ci,
                                          ci, ci, ci, ci, cf, vp, ctypes.c_size_t, vp]
     lib.attn_decode_paged_q8.restype = ci
-    i64, st, sz = ctypes.c_int64, ctypes.POINTER(_Strides), ctypes.c_size_t
+    i64, st, sz = ctypes.c_int64, vp, ctypes.c_size_t  # st: attn_strides_t, three int64
     lib.attn_kv_write_paged_q8.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, ci, vp, vp,
                                            vp, ci, ci, ci, ci, ci, ci, ci, ci, vp]
     lib.attn_kv_write_paged_q8.restype = ci
@@ -171,7 +166,8 @@ def version() -> str:
 
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    # (current_stream(device).cuda_stream makes a Stream object on the way: 2.4 us a call.)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _check(t: torch.Tensor, name: str, dtype, ndim: int):
@@ -202,6 +198,28 @@ def _same_device(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError("%s is on %s but q is on %s" % (name, t.device, device))
+
+
+def _is(t, dtype, ndim: int, index: int) -> bool:
+    """Whether a tensor is a dense one of this type and rank on this GPU: what _check and
+    _same_device ask, in a few attribute reads (they name what is wrong where it is not)."""
+    return (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.get_device() == index)
+
+
+class _OnDevice:
+    """The current CUDA device for one call, switched only where it is another."""
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.back != self.index:
+            torch.cuda.set_device(self.back)
 
 
 def _raise(rc: int, what: str):
@@ -576,29 +594,38 @@ def _q8_cache(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
                         ("k_scales", k_scales, 2), ("v_scales", v_scales, 2),
                         ("block_table", block_table, 2), ("seq_lens", seq_lens, 1),
                         ("cu_q", cu_q, 1)):
-        _dims(t, name, nd)
-    num_pages, Hkv, page_size, d = k_pages.shape
+        if not isinstance(t, torch.Tensor) or t.dim() != nd:
+            _dims(t, name, nd)
+    shape, table = k_pages.shape, block_table.shape
+    num_pages, Hkv, page_size, d = shape
     S = seq_lens.shape[0]
-    if v_pages.shape != k_pages.shape:
+    if v_pages.shape != shape:
         raise ValueError("v_pages must match k_pages, [num_pages, Hkv, page_size, d]")
-    if k_scales.shape != (num_pages, Hkv) or v_scales.shape != (num_pages, Hkv):
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
         raise ValueError("scales must be [num_pages, Hkv]")
-    if block_table.shape[0] != S or cu_q.shape[0] != S + 1:
+    if table[0] != S or cu_q.shape[0] != S + 1:
         raise ValueError("block_table needs S rows and cu_q S+1 entries")
-    return num_pages, Hkv, page_size, d, S, block_table.shape[1]
+    return num_pages, Hkv, page_size, d, S, table[1]
 
 
-def _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format):
+def _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format,
+              device):
+    index = device.index
+    codes = _KV_DTYPES[kv_format]
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype not in _KV_DTYPES[kv_format]:
-            raise TypeError("%s must be one of %s for kv_format %r"
-                            % (name, _KV_DTYPES[kv_format], kv_format))
-        _check(t, name, t.dtype, 4)
-    _check(k_scales, "k_scales", torch.float32, 2)
-    _check(v_scales, "v_scales", torch.float32, 2)
-    _check(block_table, "block_table", torch.int32, 2)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
-    _check(cu_q, "cu_q", torch.int32, 1)
+        if t.dtype not in codes:
+            raise TypeError("%s must be one of %s for kv_format %r" % (name, codes, kv_format))
+        if not _is(t, t.dtype, 4, index):
+            _check(t, name, t.dtype, 4)
+            _same_device(device, **{name: t})
+    for name, t, dtype, nd in (("k_scales", k_scales, torch.float32, 2),
+                               ("v_scales", v_scales, torch.float32, 2),
+                               ("block_table", block_table, torch.int32, 2),
+                               ("seq_lens", seq_lens, torch.int32, 1),
+                               ("cu_q", cu_q, torch.int32, 1)):
+        if not _is(t, dtype, nd, index):
+            _check(t, name, dtype, nd)
+            _same_device(device, **{name: t})
 
 
 def attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
@@ -618,21 +645,22 @@ def attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_tab
         k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
     for name, t in (("k", k), ("v", v)):
         _dims(t, name, 3)
-        if tuple(t.shape[1:]) != (Hkv, d) or t.shape[0] != k.shape[0]:
-            raise ValueError("k and v must be [T, Hkv, d] as the pages are")
-    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
-    strides = []
-    for name, t in (("k", k), ("v", v)):
-        _rows(t, name, torch.bfloat16)
-        strides.append(_row_strides(t))
-    _same_device(k.device, v=v, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales,
-                 v_scales=v_scales, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q)
-    with torch.cuda.device(k.device):
+    T = k.shape[0]
+    if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
+        raise ValueError("k and v must be [T, Hkv, d] as the pages are")
+    _rows(k, "k", torch.bfloat16)
+    _rows(v, "v", torch.bfloat16)
+    device = k.device
+    _same_device(device, v=v)
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device)
+    kh, kt = _row_strides(k)
+    vh, vt = _row_strides(v)
+    with _OnDevice(device.index):
         rc = library().attn_kv_write_paged_q8(
-            k.data_ptr(), strides[0][1], strides[0][0], v.data_ptr(), strides[1][1], strides[1][0],
-            k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-            KV_FORMATS[kv_format], block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S,
-            Hkv, k.shape[0], int(max_q), d, page_size, max_blocks, num_pages, _stream(k))
+            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, k_pages.data_ptr(), v_pages.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), KV_FORMATS[kv_format],
+            block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S, Hkv, T, int(max_q), d,
+            page_size, max_blocks, num_pages, _stream(k))
     _raise(rc, "attn_kv_write_paged_q8")
 
 
@@ -656,14 +684,17 @@ def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq
             _dims(t, name, 3)
             if tuple(t.shape) != shape:
                 raise ValueError("k and v must be [tokens, Hkv, d]")
-    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
-    k = torch.empty(shape, dtype=dtype, device=k_pages.device) if k is None else k
-    v = torch.empty(shape, dtype=dtype, device=k_pages.device) if v is None else v
-    _check(k, "k", dtype, 3)
-    _check(v, "v", dtype, 3)
-    _same_device(k_pages.device, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales,
-                 block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, k=k, v=v)
-    with torch.cuda.device(k_pages.device):
+    device = k_pages.device
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device)
+    if k is None:
+        k = k_pages.new_empty(shape, dtype=dtype)
+    if v is None:
+        v = k_pages.new_empty(shape, dtype=dtype)
+    for name, t in (("k", k), ("v", v)):
+        if not _is(t, dtype, 3, device.index):
+            _check(t, name, dtype, 3)
+            _same_device(device, **{name: t})
+    with _OnDevice(device.index):
         rc = library().attn_kv_read_paged_q8(
             k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
             KV_FORMATS[kv_format], block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
@@ -702,7 +733,8 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
         if alibi_slopes.numel() != Hq:
             raise ValueError("alibi_slopes needs one value per query head")
     _check(q, "q", torch.bfloat16, 3)
-    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
+    device = q.device
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out, lse = _decode_outputs(q, T, Hq, out, lse)
@@ -712,13 +744,11 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
         slopes_ptr = alibi_slopes.data_ptr()
     need = prefill_q8_workspace_bytes(S, Hq, Hkv, T, int(max_q), d, max_blocks, page_size)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(need, dtype=torch.uint8)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, 1)
-    _same_device(q.device, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales,
-                 block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, out=out, lse=lse,
-                 alibi_slopes=alibi_slopes, workspace=workspace)
-    with torch.cuda.device(q.device):
+    _same_device(device, out=out, lse=lse, alibi_slopes=alibi_slopes, workspace=workspace)
+    with _OnDevice(device.index):
         rc = library().attn_prefill_paged_q8(
             q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
             v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
@@ -779,14 +809,27 @@ def _rows(t, name: str, dtype):
 def _row_strides(t):
     """(head, token) strides of a [T, H, d] tensor, 0 along an extent of one (where torch may
     report any number)."""
-    return (t.stride(1) if t.shape[1] > 1 else 0, t.stride(0) if t.shape[0] > 1 else 0)
+    (T, H, _), (token, head, _) = t.shape, t.stride()
+    return head if H > 1 else 0, token if T > 1 else 0
 
 
-def _strides(t):
-    if t.dim() == 3:
-        head, token = _row_strides(t)
-        return _Strides(0, head, token)
-    return _Strides(*(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)))
+def _strides(*tensors):
+    """The attn_strides_t of each tensor as addresses (None for None), and the array that holds
+    them: keep it until the call."""
+    flat, at = [], []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        at.append(len(flat) * 8)
+        n, st = t.shape, t.stride()
+        if len(n) == 3:
+            flat += (0, st[1] if n[1] > 1 else 0, st[0] if n[0] > 1 else 0)
+        else:
+            flat += (st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0)
+    held = (ctypes.c_int64 * len(flat))(*flat)
+    base = ctypes.addressof(held)
+    return [None if a is None else base + a for a in at], held
 
 
 def _rope_args(q, k, positions, inv_freq, like_q, like_k):
@@ -794,25 +837,32 @@ def _rope_args(q, k, positions, inv_freq, like_q, like_k):
     (or None) that must look like q and k.  Returns B, Hq, Hkv, N, d and the position stride."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    nd = q.dim()
-    if nd not in (3, 4):
+    nd, qs = q.dim(), q.shape
+    if nd == 3:
+        N, Hq, d = qs
+        B = 1
+    elif nd == 4:
+        B, Hq, N, d = qs
+    else:
         raise ValueError("q must be [B, Hq, N, d] or token-major [T, Hq, d], got shape %s"
-                         % (tuple(q.shape),))
+                         % (tuple(qs),))
+    Hkv = 0
     if k is not None:
         _dims(k, "k", nd)
-        if nd == 4 and (k.shape[0], k.shape[2], k.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]):
-            raise ValueError("k must be [B, Hkv, N, d] matching q %s" % (tuple(q.shape),))
-        if nd == 3 and (k.shape[0], k.shape[2]) != (q.shape[0], q.shape[2]):
-            raise ValueError("k must be [T, Hkv, d] matching q %s" % (tuple(q.shape),))
+        ks = k.shape
+        Hkv = ks[1]
+        if ks != ((N, Hkv, d) if nd == 3 else (B, Hkv, N, d)):
+            raise ValueError("k must be %s matching q %s"
+                             % ("[T, Hkv, d]" if nd == 3 else "[B, Hkv, N, d]", tuple(qs)))
     elif any(t is not None for _, t in like_k):
         raise ValueError("%s given without k" % like_k[0][0])
     if not isinstance(positions, torch.Tensor) or not isinstance(inv_freq, torch.Tensor):
         raise TypeError("positions and inv_freq must be torch.Tensors")
-    B, N = (1, q.shape[0]) if nd == 3 else (q.shape[0], q.shape[2])
-    if tuple(positions.shape) != (N,) and (nd == 3 or tuple(positions.shape) != (B, N)):
+    ps = positions.shape
+    if ps != (N,) and (nd == 3 or ps != (B, N)):
         raise ValueError("positions must be [T] or [N], or [B, N] with a batch")
     _dims(inv_freq, "inv_freq", 1)
-    if not 1 <= inv_freq.shape[0] <= q.shape[-1] // 2:
+    if not 1 <= inv_freq.shape[0] <= d // 2:
         raise ValueError("inv_freq needs one value per pair, at most d/2")
     for like, ref, what in ((like_q, q, "q"), (like_k, k, "k")):
         for name, t in like:
@@ -820,32 +870,30 @@ def _rope_args(q, k, positions, inv_freq, like_q, like_k):
                 _dims(t, name, nd)
                 if t.shape != ref.shape:
                     raise ValueError("%s must have %s's shape" % (name, what))
-    if q.dtype not in _DTYPES:
-        raise TypeError("q must be bfloat16 or float32, got %s" % q.dtype)
-    _rows(q, "q", q.dtype)
+    dtype, device = q.dtype, q.device
+    if dtype not in _DTYPES:
+        raise TypeError("q must be bfloat16 or float32, got %s" % dtype)
+    _rows(q, "q", dtype)
     if k is not None:
-        _rows(k, "k", q.dtype)
+        _rows(k, "k", dtype)
+        _same_device(device, k=k)
     for name, t in like_q + like_k:
         if t is not None:
-            _rows(t, name, q.dtype)
-    _check(positions, "positions", torch.int32, positions.dim())
-    _check(inv_freq, "inv_freq", torch.float64, 1)
-    _same_device(q.device, k=k, positions=positions, inv_freq=inv_freq,
-                 **dict(like_q + like_k))
-    Hkv = 0 if k is None else k.shape[1]
-    return B, q.shape[1], Hkv, N, q.shape[-1], N if positions.dim() == 2 else 0
+            _rows(t, name, dtype)
+            _same_device(device, **{name: t})
+    for name, t, dt in (("positions", positions, torch.int32), ("inv_freq", inv_freq, torch.float64)):
+        if not _is(t, dt, t.dim(), device.index):
+            _check(t, name, dt, t.dim())
+            _same_device(device, **{name: t})
+    return B, Hq, Hkv, N, d, N if len(ps) == 2 else 0
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _ref(t):
-    return None if t is None else ctypes.byref(_strides(t))
-
-
 def _empty_rows(t):
-    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def attn_rope(q, k, positions, inv_freq, interleaved: bool = False, attention_factor: float = 1.0,
@@ -865,10 +913,10 @@ def attn_rope(q, k, positions, inv_freq, interleaved: bool = False, attention_fa
                                               [("k_out", k_out)])
     q_out = _empty_rows(q) if q_out is None else q_out
     k_out = _empty_rows(k) if k_out is None else k_out
-    with torch.cuda.device(q.device):
-        rc = library().attn_rope(_ptr(q), _ref(q), _ptr(q_out), _ref(q_out), _ptr(k), _ref(k),
-                                 _ptr(k_out), _ref(k_out), positions.data_ptr(), pos_stride,
-                                 inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N, d,
+    st, held = _strides(q, q_out, k, k_out)
+    with _OnDevice(q.get_device()):
+        rc = library().attn_rope(_ptr(q), st[0], _ptr(q_out), st[1], _ptr(k), st[2], _ptr(k_out),
+                                 st[3], positions.data_ptr(), pos_stride, inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N, d,
                                  2 * inv_freq.shape[0], int(bool(interleaved)),
                                  float(attention_factor), int(bool(transpose)), _stream(q))
     _raise(rc, "attn_rope")
@@ -883,8 +931,9 @@ def _norm_weights(q, k, q_weight, k_weight):
             _dims(t, name, 1)
             if t.shape[0] != q.shape[-1]:
                 raise ValueError("%s must be [d]" % name)
-            _check(t, name, q.dtype, 1)
-    _same_device(q.device, q_weight=q_weight, k_weight=k_weight)
+            if not _is(t, q.dtype, 1, q.get_device()):
+                _check(t, name, q.dtype, 1)
+                _same_device(q.device, **{name: t})
 
 
 def attn_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6,
@@ -900,9 +949,10 @@ def attn_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1
     _norm_weights(q, k, q_weight, k_weight)
     q_out = _empty_rows(q) if q_out is None else q_out
     k_out = _empty_rows(k) if k_out is None else k_out
-    with torch.cuda.device(q.device):
-        rc = library().attn_norm_rope(_ptr(q), _ref(q), _ptr(q_weight), _ptr(q_out), _ref(q_out),
-                                      _ptr(k), _ref(k), _ptr(k_weight), _ptr(k_out), _ref(k_out),
+    st, held = _strides(q, q_out, k, k_out)
+    with _OnDevice(q.get_device()):
+        rc = library().attn_norm_rope(_ptr(q), st[0], _ptr(q_weight), _ptr(q_out), st[1], _ptr(k),
+                                      st[2], _ptr(k_weight), _ptr(k_out), st[3],
                                       positions.data_ptr(), pos_stride, inv_freq.data_ptr(),
                                       _DTYPES[q.dtype], B, Hq, Hkv, N, d, 2 * inv_freq.shape[0],
                                       int(bool(interleaved)), float(attention_factor), float(eps),
@@ -933,30 +983,35 @@ def attn_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, positions, inv_
                                               [("dq_out", dq_out), ("dq", dq)],
                                               [("dk_out", dk_out), ("dk", dk)])
     _norm_weights(q, k, q_weight, k_weight)
+    index = q.get_device()
+    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if t is not None:
+            _dims(t, name, 1)
+            if t.shape[0] != d or k is None and name == "dk_weight":
+                raise ValueError("%s must be [d], and None without k" % name)
+            if not _is(t, torch.float32, 1, index):
+                _check(t, name, torch.float32, 1)
+                _same_device(q.device, **{name: t})
     dq = _empty_rows(q) if dq is None else dq
     dk = _empty_rows(k) if dk is None else dk
     if dq_weight is None:
-        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
+        dq_weight = q.new_empty(d, dtype=torch.float32)
     if dk_weight is None and k is not None:
-        dk_weight = torch.empty(d, dtype=torch.float32, device=q.device)
-    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
-        if t is not None:
-            _check(t, name, torch.float32, 1)
-            if t.shape[0] != d or k is None and name == "dk_weight":
-                raise ValueError("%s must be [d], and None without k" % name)
-    need = norm_rope_bwd_workspace_bytes(B, Hq, Hkv, N, d)
+        dk_weight = q.new_empty(d, dtype=torch.float32)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    _check(workspace, "workspace", torch.uint8, 1)
-    _same_device(q.device, dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace)
-    with torch.cuda.device(q.device):
+        need = norm_rope_bwd_workspace_bytes(B, Hq, Hkv, N, d)
+        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
+    elif not _is(workspace, torch.uint8, 1, index):
+        _check(workspace, "workspace", torch.uint8, 1)
+        _same_device(q.device, workspace=workspace)
+    st, held = _strides(q, dq_out, dq, k, dk_out, dk)
+    with _OnDevice(index):
         rc = library().attn_norm_rope_bwd(
-            _ptr(q), _ref(q), _ptr(q_weight), _ptr(dq_out), _ref(dq_out), _ptr(dq), _ref(dq),
-            _ptr(dq_weight), _ptr(k), _ref(k), _ptr(k_weight), _ptr(dk_out), _ref(dk_out),
-            _ptr(dk), _ref(dk), _ptr(dk_weight), positions.data_ptr(), pos_stride,
-            inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N, d, 2 * inv_freq.shape[0],
-            int(bool(interleaved)), float(attention_factor), float(eps), workspace.data_ptr(),
-            workspace.numel(), _stream(q))
+            _ptr(q), st[0], _ptr(q_weight), _ptr(dq_out), st[1], _ptr(dq), st[2], _ptr(dq_weight),
+            _ptr(k), st[3], _ptr(k_weight), _ptr(dk_out), st[4], _ptr(dk), st[5], _ptr(dk_weight),
+            positions.data_ptr(), pos_stride, inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N,
+            d, 2 * inv_freq.shape[0], int(bool(interleaved)), float(attention_factor), float(eps),
+            workspace.data_ptr(), workspace.numel(), _stream(q))
     _raise(rc, "attn_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
 
