@@ -15,27 +15,32 @@
 // written once, and the arithmetic of a row is about 100 operations per 16
 // elements.  So:
 //  * One thread holds the same 16 elements (8 pairs) of its rows and walks the
-//    heads of one token: the cosines and sines of its 8 pairs and its weights
+//    heads of one token, q's and then k's: the cosines and sines of its 8 pairs
 //    stay in registers, worked out once for all those heads.  LPR = d/16 lanes
 //    hold a row, and a norm's two sums are log2(LPR) shuffles.
-//  * Each lane moves 16-byte words, and kUnroll rows are loaded before the
-//    first is used.  Half layouts whose rot is not a multiple of 16 would put
-//    the partner elements at odd addresses: they go element by element.
-//  * q and k go in one launch; each block works on heads of one of the two.
+//  * Each lane moves 16-byte words, and the next kAhead rows are on their way,
+//    packed as they lie in memory, while a row is worked on.  (Four rows loaded
+//    and unpacked together took 128 registers: 95 us for 4 x 4096 tokens of 40
+//    bf16 heads with norms, and 197 us for the gradient.)  Half layouts whose rot
+//    is not a multiple of two such words would put the partner elements at odd
+//    addresses: they go element by element.
 //  * Angles: t * f_i / 2 pi is taken in 64 bits and reduced to the nearest
 //    whole turn there (a far position's angle has no fraction left in 32
 //    bits); the remainder, at most half a turn, goes to sincospi in 32 bits.
 //    One 64-bit product serves all heads of the token.
 //  * Sums, norms and products are float32, rounded once when a row is stored.
-//  * The weights' gradients: each thread adds its 16 elements' products over
-//    all its rows, the block adds its lanes' sums in shared memory and writes
-//    one row of partial sums per block, and a second kernel, scheduled behind
-//    the first, adds those rows in a fixed order.  No atomics: the result does
-//    not depend on the order in which blocks run.
+//  * The weights' gradients: each thread adds its 16 elements' products over a
+//    token's heads in registers and over its tokens in shared memory, the block
+//    adds its lanes' sums and writes one row of partial sums, and a second
+//    kernel, scheduled behind the first, adds those rows in a fixed order.  No
+//    atomics: the result does not depend on the order in which blocks run.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -44,7 +49,6 @@ namespace exattn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;       // rows in flight per thread
 constexpr int kSMs = 148;
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
@@ -57,8 +61,7 @@ struct Side {
   void *y;             // output, or dx
   const void *w;       // norm weights [d]
   long long xb, xh, xn, yb, yh, yn, gb, gh, gn;  // element strides: batch, head, token
-  float *dw;           // float32 [d] (gradient)
-  int H, groups, per_group;
+  int H;
 };
 
 struct RopeParams {
@@ -66,103 +69,133 @@ struct RopeParams {
   const int *positions;
   long long pos_stride;  // of a batch entry; 0: shared
   const double *inv_freq;
-  float *partial;  // gradient: [blocks][d], block (x, y) at row y * gridDim.x + x
+  float *partial;  // gradient: [2][blocks][d], block (x, y) at row y * gridDim.x + x
   long long tokens;
   int N, rot;
+  int per_group;  // heads (q's and k's together) of a block
   float factor, sign, eps;
 };
 
+// One 16-byte word of elements as floats, and back.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Word {
+  static constexpr int L = 16 / sizeof(T);  // elements
+  static __device__ __forceinline__ void get(const uint4 &u, float *v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        v[i] = __uint_as_float(w[i]);
+      }
+    }
   }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
-  *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+  static __device__ __forceinline__ uint4 put(const float *v) {
+    if constexpr (sizeof(T) == 2)
+      return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                        pack_bf16x2(v[6], v[7]));
+    else
+      return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                        __float_as_uint(v[3]));
+  }
+};
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void from_f32(float *p, float v) { *p = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The 16 elements of a row that belong to lane `i` of its LPR lanes, as 8
-// slots (a[j], b[j]).  Slots are numbered 0 .. d/2-1; slot s < rot/2 is pair s,
-// and slot s >= rot/2 the two unturned elements 2s and 2s+1.  kHalf and kPairs:
-// lane i holds slots 8i .. 8i+7; in the half layout with rot % 16 == 0 they are
-// either 8 pairs, two runs of 8 elements rot/2 apart, or 16 unturned ones; in
-// the interleaved layout always 16 elements in a row.  kScalar: slots i + LPR*j.
-template <int D, int MODE>
+// The 16 elements of a row that belong to lane `lane` of its LPR lanes, as 8
+// slots (a[j], b[j]).  Slots of a row are numbered 0 .. d/2-1; slot s < rot/2 is
+// pair s, and slot s >= rot/2 the two unturned elements 2s and 2s+1.
+//  kHalf, kPairs: groups of G slots in a row, group g of all lanes side by side
+//  before group g + 1 of any, so that the lanes' 16-byte words lie side by side
+//  too.  In the half layout a group that turns is two words rot/2 elements
+//  apart (rot/2 a multiple of G, so it turns as a whole), in the interleaved
+//  layout every group is one word.  kScalar: slots lane + LPR * j, any rot.
+template <typename T, int D, int MODE>
 struct Slots {
   static constexpr int LPR = D / 16;
-  int o0, o1;    // kHalf, kPairs: first elements of the two runs of 8
-  int nturn;     // kHalf, kPairs: slots j < nturn turn
+  static constexpr int L = Word<T>::L;
+  static constexpr int G = MODE == kPairs ? L / 2 : L;
+  static constexpr int W = MODE == kScalar ? 1 : 16 / L;  // words of a row's share
+  // A row's share as it was loaded.
+  struct Words {
+    uint4 w[W];
+  };
+  struct Single {
+    T a[8], b[8];
+  };
+  using Held = typename std::conditional<MODE == kScalar, Single, Words>::type;
   int lane, half;
+  int at[W];  // elements where the words begin
   __device__ __forceinline__ Slots(int lane_, int rot) : lane(lane_), half(rot >> 1) {
-    const bool pair_runs = MODE == kHalf && 8 * lane < half;
-    o0 = pair_runs ? 8 * lane : 16 * lane;
-    o1 = pair_runs ? half + 8 * lane : 16 * lane + 8;
-    nturn = min(8, max(0, half - 8 * lane));
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (MODE == kPairs) at[w] = 2 * slot(w * G);
+      else at[w] = w & 1 ? second((w >> 1) * G) : first((w >> 1) * G);
+    }
   }
-  __device__ __forceinline__ int slot(int j) const { return MODE == kScalar ? lane + LPR * j : 8 * lane + j; }
-  __device__ __forceinline__ bool turns(int j) const { return MODE == kScalar ? slot(j) < half : j < nturn; }
-  __device__ __forceinline__ int first(int j) const {  // kScalar: element of a[j]
+  __device__ __forceinline__ int slot(int j) const {
+    return MODE == kScalar ? lane + LPR * j : (j / G) * (G * LPR) + G * lane + j % G;
+  }
+  __device__ __forceinline__ bool turns(int j) const {
+    return (MODE == kHalf ? slot(j - j % G) : slot(j)) < half;
+  }
+  __device__ __forceinline__ int first(int j) const {  // element of a[j] (half layouts)
     const int s = slot(j);
-    return s < half ? s : 2 * s;
+    if (MODE == kScalar) return s < half ? s : 2 * s;
+    return turns(j) ? s : 2 * slot(j - j % G) + j % G;
   }
   __device__ __forceinline__ int second(int j) const {
     const int s = slot(j);
-    return s < half ? s + half : 2 * s + 1;
+    if (MODE == kScalar) return s < half ? s + half : 2 * s + 1;
+    return turns(j) ? s + half : 2 * slot(j - j % G) + G + j % G;
   }
-  // Element of the weights' gradient that slot j's a (which = 0) or b holds.
+  // The element that slot j's a (which = 0) or b holds.
   __device__ __forceinline__ int element(int j, int which) const {
-    if (MODE == kScalar) return which ? second(j) : first(j);
-    if (MODE == kPairs) return 16 * lane + 2 * j + which;
-    return (which ? o1 : o0) + j;
+    if (MODE == kPairs) return 2 * slot(j) + which;
+    return which ? second(j) : first(j);
   }
-  template <typename T>
-  __device__ __forceinline__ void load(const T *row, float (&a)[8], float (&b)[8]) const {
+  __device__ __forceinline__ void load(const T *row, Held &r) const {
     if constexpr (MODE == kScalar) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        a[j] = to_f32(row[first(j)]);
-        b[j] = to_f32(row[second(j)]);
+        r.a[j] = row[first(j)];
+        r.b[j] = row[second(j)];
       }
     } else {
-      float u[8], v[8];
-      load8(row + o0, u);
-      load8(row + o1, v);
+#pragma unroll
+      for (int w = 0; w < W; ++w) r.w[w] = *reinterpret_cast<const uint4 *>(row + at[w]);
+    }
+  }
+  __device__ __forceinline__ void get(const Held &r, float (&a)[8], float (&b)[8]) const {
+    if constexpr (MODE == kScalar) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if constexpr (MODE == kHalf) {
-          a[j] = u[j];
-          b[j] = v[j];
-        } else {
-          a[j] = j < 4 ? u[(2 * j) & 7] : v[(2 * j) & 7];
-          b[j] = j < 4 ? u[(2 * j + 1) & 7] : v[(2 * j + 1) & 7];
+        a[j] = to_f32(r.a[j]);
+        b[j] = to_f32(r.b[j]);
+      }
+    } else if constexpr (MODE == kHalf) {
+#pragma unroll
+      for (int g = 0; g < 8 / G; ++g) {
+        Word<T>::get(r.w[2 * g], a + g * G);
+        Word<T>::get(r.w[2 * g + 1], b + g * G);
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 8 / G; ++g) {
+        float v[L];
+        Word<T>::get(r.w[g], v);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          a[g * G + i] = v[2 * i];
+          b[g * G + i] = v[2 * i + 1];
         }
       }
     }
   }
-  template <typename T>
   __device__ __forceinline__ void store(T *row, const float (&a)[8], const float (&b)[8]) const {
     if constexpr (MODE == kScalar) {
 #pragma unroll
@@ -170,23 +203,23 @@ struct Slots {
         from_f32(row + first(j), a[j]);
         from_f32(row + second(j), b[j]);
       }
-    } else {
-      float u[8], v[8];
+    } else if constexpr (MODE == kHalf) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (MODE == kHalf) {
-          u[j] = a[j];
-          v[j] = b[j];
-        } else if (j < 4) {
-          u[(2 * j) & 7] = a[j];
-          u[(2 * j + 1) & 7] = b[j];
-        } else {
-          v[(2 * j) & 7] = a[j];
-          v[(2 * j + 1) & 7] = b[j];
-        }
+      for (int g = 0; g < 8 / G; ++g) {
+        *reinterpret_cast<uint4 *>(row + at[2 * g]) = Word<T>::put(a + g * G);
+        *reinterpret_cast<uint4 *>(row + at[2 * g + 1]) = Word<T>::put(b + g * G);
       }
-      store8(row + o0, u);
-      store8(row + o1, v);
+    } else {
+#pragma unroll
+      for (int g = 0; g < 8 / G; ++g) {
+        float v[L];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          v[2 * i] = a[g * G + i];
+          v[2 * i + 1] = b[g * G + i];
+        }
+        *reinterpret_cast<uint4 *>(row + at[g]) = Word<T>::put(v);
+      }
     }
   }
 };
@@ -199,24 +232,31 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Block (x, y): group y of heads of one tensor, token tiles x, x + gridDim.x, ...
-template <typename T, int D, int MODE, int OP>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-  constexpr int LPR = D / 16, TT = kThreads / LPR;
-  if constexpr (OP == kNormTurnBwd) grid_dependents_launch();
-  const int lane = threadIdx.x % LPR, slot_row = threadIdx.x / LPR;
-  const int which = blockIdx.y < p.side[0].groups ? 0 : 1;
-  const Side &sd = p.side[which];
-  const int group = blockIdx.y - (which ? p.side[0].groups : 0);
-  const int h0 = group * sd.per_group, h1 = min(sd.H, h0 + sd.per_group);
-  const Slots<D, MODE> sl(lane, p.rot);
+// Blocks that an SM holds at a time (the registers' limit is set to that), and
+// rows on their way while one is worked on: more of either spills.
+constexpr int blocks_per_sm(int op, int size) {
+  return op == kTurn ? 7 : (op == kNormTurn ? 5 : (size == 4 ? 3 : 4));
+}
+constexpr int rows_ahead(int mode, int op, int size) {
+  return op == kNormTurnBwd || mode == kScalar || size == 4 ? 1 : 2;
+}
 
-  float wa[8], wb[8];  // norm weights of this lane's elements
-  if constexpr (OP != kTurn) sl.load(static_cast<const T *>(sd.w), wa, wb);
-  float ga[8], gb[8];  // their gradients, over this thread's rows
-  if constexpr (OP == kNormTurnBwd) {
+// Block (x, y): group y of the heads, token tiles x, x + gridDim.x, ...
+template <typename T, int D, int MODE, int OP>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(OP, sizeof(T))) rope_kernel(const RopeParams p) {
+  constexpr int LPR = D / 16, TT = kThreads / LPR;
+  constexpr int A = rows_ahead(MODE, OP, sizeof(T));
+  constexpr bool kBwd = OP == kNormTurnBwd;
+  if constexpr (kBwd) grid_dependents_launch();
+  using S = Slots<T, D, MODE>;
+  const int lane = threadIdx.x % LPR, slot_row = threadIdx.x / LPR;
+  const S sl(lane, p.rot);
+  const int hb = blockIdx.y * p.per_group, he = hb + p.per_group;
+  // Gradient: this thread's sums of its 16 elements' dw, for q and for k.
+  __shared__ float sums[kBwd ? 2 : 1][kBwd ? 16 : 1][kThreads];
+  if constexpr (kBwd) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ga[j] = gb[j] = 0.f;
+    for (int j = 0; j < 16; ++j) sums[0][j][threadIdx.x] = sums[1][j][threadIdx.x] = 0.f;
   }
 
   for (long long tile = blockIdx.x; tile * TT < p.tokens; tile += gridDim.x) {
@@ -241,93 +281,142 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
         }
       }
     }
-    auto turn = [&](float &a, float &b, int j) {
-      const float y = a * cs[j] - b * sn[j], z = a * sn[j] + b * cs[j];
-      // (Not by cos 1, sin 0 for the rest: an infinity beside it would turn to NaN.)
-      a = sl.turns(j) ? y : a;
-      b = sl.turns(j) ? z : b;
-    };
-    const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + n * sd.xn;
-    T *y = static_cast<T *>(sd.y) + bi * sd.yb + n * sd.yn;
-    const T *dy = OP == kNormTurnBwd ? static_cast<const T *>(sd.dy) + bi * sd.gb + n * sd.gn : nullptr;
-    constexpr int U = OP == kNormTurnBwd ? 2 : kUnroll;
-    for (int h = h0; h < h1; h += U) {
-      float a[U][8], b[U][8], c[OP == kNormTurnBwd ? U : 1][8], e[OP == kNormTurnBwd ? U : 1][8];
+    // Turns the 8 slots of a row.  (What does not turn is left alone, not turned
+    // by cosine 1 and sine 0: an infinity would make its neighbour NaN.)
+    auto turn = [&](float (&a)[8], float (&b)[8]) {
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (h + i < h1) {
-          sl.load(x + (h + i) * sd.xh, a[i], b[i]);
-          if constexpr (OP == kNormTurnBwd) sl.load(dy + (h + i) * sd.gh, c[i], e[i]);
+      for (int g = 0; g < 8; g += S::G) {
+        if (MODE == kHalf && !sl.turns(g)) continue;  // here a group turns as a whole
+#pragma unroll
+        for (int j = g; j < g + S::G; ++j) {
+          const float y = a[j] * cs[j] - b[j] * sn[j], z = a[j] * sn[j] + b[j] * cs[j];
+          const bool t = MODE == kHalf || sl.turns(j);
+          a[j] = t ? y : a[j];
+          b[j] = t ? z : b[j];
         }
+      }
+    };
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const Side &sd = p.side[side];
+      const int off = side ? p.side[0].H : 0;
+      const int h0 = max(hb - off, 0), h1 = min(he - off, sd.H);
+      if (h0 >= h1) continue;
+      float wa[8], wb[8];  // norm weights of this lane's elements
+      if constexpr (OP != kTurn) {
+        typename S::Held w;
+        sl.load(static_cast<const T *>(sd.w), w);
+        sl.get(w, wa, wb);
+      }
+      float ga[8], gb[8];  // their gradients, over this token's heads
+      if constexpr (kBwd) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (h + i >= h1) break;  // (the same for every lane)
-        if constexpr (OP == kTurn) {
+        for (int j = 0; j < 8; ++j) ga[j] = gb[j] = 0.f;
+      }
+      const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + n * sd.xn;
+      T *y = static_cast<T *>(sd.y) + bi * sd.yb + n * sd.yn;
+      const T *dy = kBwd ? static_cast<const T *>(sd.dy) + bi * sd.gb + n * sd.gn : nullptr;
+      typename S::Held xr[A], gr[kBwd ? A : 1];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) turn(a[i][j], b[i][j], j);
-        } else {
-          float ss = 0.f;
+      for (int i = 0; i < A; ++i)
+        if (h0 + i < h1) {
+          sl.load(x + (h0 + i) * sd.xh, xr[i]);
+          if constexpr (kBwd) sl.load(dy + (h0 + i) * sd.gh, gr[i]);
+        }
+      for (int hh = h0; hh < h1; hh += A) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss += a[i][j] * a[i][j] + b[i][j] * b[i][j];
-          const float r = __frsqrt_rn(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-          if constexpr (OP == kNormTurn) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              a[i][j] = a[i][j] * r * wa[j];
-              b[i][j] = b[i][j] * r * wb[j];
-              turn(a[i][j], b[i][j], j);
-            }
+        for (int i = 0; i < A; ++i) {
+          const int h = hh + i;
+          if (h >= h1) break;  // (the same for every lane)
+          float a[8], b[8], c[kBwd ? 8 : 1], e[kBwd ? 8 : 1];
+          sl.get(xr[i], a, b);
+          if constexpr (kBwd) sl.get(gr[i], c, e);
+          // (In place, a row's lanes store after all of them have loaded it; the
+          // rows on their way are other rows.)
+          if (h + A < h1) {
+            sl.load(x + (h + A) * sd.xh, xr[i]);
+            if constexpr (kBwd) sl.load(dy + (h + A) * sd.gh, gr[i]);
+          }
+          if constexpr (OP == kTurn) {
+            turn(a, b);
           } else {
-            float dot = 0.f;
+            float ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              turn(c[i][j], e[i][j], j);  // u: sign is -1 here
-              a[i][j] *= r;               // xhat
-              b[i][j] *= r;
-              if (live) {
-                ga[j] += c[i][j] * a[i][j];
-                gb[j] += e[i][j] * b[i][j];
+            for (int j = 0; j < 8; ++j) ss += a[j] * a[j] + b[j] * b[j];
+            const float r = __frsqrt_rn(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+            if constexpr (OP == kNormTurn) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                a[j] = a[j] * r * wa[j];
+                b[j] = b[j] * r * wb[j];
               }
-              c[i][j] *= wa[j];
-              e[i][j] *= wb[j];
-              dot += c[i][j] * a[i][j] + e[i][j] * b[i][j];
-            }
-            dot = row_sum<LPR>(dot) * (1.f / D);
+              turn(a, b);
+            } else {
+              float dot = 0.f;
+              turn(c, e);  // u: sign is -1 here
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              a[i][j] = r * (c[i][j] - a[i][j] * dot);
-              b[i][j] = r * (e[i][j] - b[i][j] * dot);
+              for (int j = 0; j < 8; ++j) {
+                a[j] *= r;  // xhat
+                b[j] *= r;
+                ga[j] += c[j] * a[j];
+                gb[j] += e[j] * b[j];
+                c[j] *= wa[j];
+                e[j] *= wb[j];
+                dot += c[j] * a[j] + e[j] * b[j];
+              }
+              dot = row_sum<LPR>(dot) * (1.f / D);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                a[j] = r * (c[j] - a[j] * dot);
+                b[j] = r * (e[j] - b[j] * dot);
+              }
             }
           }
+          if (live) sl.store(y + h * sd.yh, a, b);
         }
-        if (live) sl.store(y + (h + i) * sd.yh, a[i], b[i]);
+      }
+      if constexpr (kBwd) {
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sums[side][j][threadIdx.x] += ga[j];
+            sums[side][8 + j][threadIdx.x] += gb[j];
+          }
+        }
       }
     }
   }
 
-  if constexpr (OP == kNormTurnBwd) {
-    // The block's rows of sums: lanes of a warp that hold the same elements
+  if constexpr (kBwd) {
+    // The block's row of sums: lanes of a warp that hold the same elements
     // first, then the warps, in a fixed order.
-    __shared__ float sums[kThreads / 32][D];
+    __shared__ float by_warp[kThreads / 32][D];
     const int warp = threadIdx.x >> 5;
+    const long long block = static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const long long blocks = static_cast<long long>(gridDim.y) * gridDim.x;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 8; ++j) {
+        float a = sums[side][j][threadIdx.x], b = sums[side][8 + j][threadIdx.x];
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) {
-        ga[j] += __shfl_xor_sync(0xffffffffu, ga[j], o);
-        gb[j] += __shfl_xor_sync(0xffffffffu, gb[j], o);
+        for (int o = LPR; o < 32; o <<= 1) {
+          a += __shfl_xor_sync(0xffffffffu, a, o);
+          b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
+        if ((threadIdx.x & 31) < LPR) {
+          by_warp[warp][sl.element(j, 0)] = a;
+          by_warp[warp][sl.element(j, 1)] = b;
+        }
       }
-      if ((threadIdx.x & 31) < LPR) {
-        sums[warp][sl.element(j, 0)] = ga[j];
-        sums[warp][sl.element(j, 1)] = gb[j];
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float s = 0.f;
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) s += sums[w][threadIdx.x];
-      p.partial[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * D + threadIdx.x] = s;
+        for (int w = 0; w < kThreads / 32; ++w) s += by_warp[w][threadIdx.x];
+        p.partial[(side * blocks + block) * D + threadIdx.x] = s;
+      }
+      __syncthreads();
     }
   }
 }
@@ -337,13 +426,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
 constexpr int kSumThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kSumThreads)
-    rope_dw_kernel(const float *partial, float *dw0, float *dw1, int rows0, int rows1) {
+    rope_dw_kernel(const float *partial, float *dw0, float *dw1, int rows) {
   grid_dependency_wait();
   const int side = blockIdx.y;
   float *dw = side ? dw1 : dw0;
-  const int rows = side ? rows1 : rows0;
   if (!dw) return;
-  const float *src = partial + (side ? static_cast<long long>(rows0) * D : 0);
+  const float *src = partial + static_cast<long long>(side) * rows * D;
   const int e = blockIdx.x * 8 + (threadIdx.x & 7), part = threadIdx.x >> 3;
   float s = 0.f;
   for (int r = part; r < rows; r += kSumThreads / 8) s += src[static_cast<long long>(r) * D + e];
@@ -359,41 +447,42 @@ __global__ void __launch_bounds__(kSumThreads)
 
 // How a call is cut into blocks: token tiles by groups of heads.
 struct Cut {
-  long long tiles;
-  int per[2], groups[2];
-  int grid_x;
+  int per, groups, grid_x;
 };
 
-Cut cut(long long tokens, int Hq, int Hkv, int d, bool bwd) {
-  Cut c;
+Cut cut(long long tokens, int heads, int d, int op, int size) {
   const int tt = kThreads / (d / 16);
-  c.tiles = (tokens + tt - 1) / tt;
-  // Heads per block: as many as leave about eight blocks for each SM (an
-  // angle then serves all of them), at most 16.
-  const long long want = c.tiles * (Hq + Hkv) / (kSMs * 8);
-  const int per = static_cast<int>(want < 1 ? 1 : (want > 16 ? 16 : want));
-  const int H[2] = {Hq, Hkv};
-  for (int i = 0; i < 2; ++i) {
-    c.groups[i] = H[i] ? (H[i] + per - 1) / per : 0;
-    c.per[i] = c.groups[i] ? (H[i] + c.groups[i] - 1) / c.groups[i] : 0;
+  const long long tiles = (tokens + tt - 1) / tt;
+  const long long slots = kSMs * blocks_per_sm(op, size);  // blocks that run at a time
+  // A block's time is about its heads plus the angles, which take as long as
+  // kAngles heads; all blocks take as many turns as they fill the slots.
+  // More groups balance the turns better and work the angles out more often.
+  constexpr int kAngles = 3;
+  Cut c{heads, 1, 0};
+  long long best = -1, turns = 1;
+  for (int g = 1; g <= heads && g <= 256; ++g) {
+    const int per = (heads + g - 1) / g;
+    const long long t = (tiles * g + slots - 1) / slots, cost = t * (per + kAngles);
+    if (best < 0 || cost < best) {
+      best = cost;
+      turns = t;
+      c.per = per;
+      c.groups = (heads + per - 1) / per;
+    }
   }
-  long long gx = c.tiles;
-  if (bwd) {
-    // A row of partial sums per block: a block takes several tiles, so that
-    // there are at most about eight blocks per SM.
-    const long long most = (kSMs * 8 + c.groups[0] + c.groups[1] - 1) / (c.groups[0] + c.groups[1]);
-    if (gx > most) gx = most;
-  }
+  // The gradient has a row of partial sums per block: there a block takes its
+  // turns itself, tile after tile.
+  const long long gx = op == kNormTurnBwd ? (tiles + turns - 1) / turns : tiles;
   c.grid_x = gx > 0x7fffffffLL ? -1 : static_cast<int>(gx);
   return c;
 }
 
 template <typename T, int D, int OP>
 attn_status_t launch_mode(const RopeParams &p, const Cut &c, bool interleaved, cudaStream_t stream) {
-  const dim3 grid(c.grid_x, c.groups[0] + c.groups[1]);
+  const dim3 grid(c.grid_x, c.groups);
   if (interleaved)
     rope_kernel<T, D, kPairs, OP><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.rot % 16 == 0)
+  else if (p.rot % (2 * Word<T>::L) == 0)
     rope_kernel<T, D, kHalf, OP><<<grid, kThreads, 0, stream>>>(p);
   else
     rope_kernel<T, D, kScalar, OP><<<grid, kThreads, 0, stream>>>(p);
@@ -413,8 +502,11 @@ attn_status_t launch_op(const RopeParams &p, const Cut &c, int dtype, int d, boo
 }  // namespace
 
 size_t norm_rope_bwd_workspace_bytes(long long tokens, int Hq, int Hkv, int d) {
-  const Cut c = cut(tokens, Hq, Hkv, d, true);
-  return static_cast<size_t>(c.grid_x) * (c.groups[0] + c.groups[1]) * d * sizeof(float);
+  // (Whichever type the call has.)
+  const Cut a = cut(tokens, Hq + Hkv, d, kNormTurnBwd, 2), b = cut(tokens, Hq + Hkv, d, kNormTurnBwd, 4);
+  const long long rows = std::max(static_cast<long long>(a.grid_x) * a.groups,
+                                   static_cast<long long>(b.grid_x) * b.groups);
+  return static_cast<size_t>(2) * rows * d * sizeof(float);
 }
 
 attn_status_t launch_rope(const RopeSide &q, const RopeSide &k, const int *positions,
@@ -424,20 +516,21 @@ attn_status_t launch_rope(const RopeSide &q, const RopeSide &k, const int *posit
   const bool bwd = op == kNormTurnBwd;
   RopeParams p{};
   p.tokens = static_cast<long long>(B) * N;
-  const Cut c = cut(p.tokens, q.H, k.H, d, bwd);
-  if (c.grid_x < 0 || c.groups[0] + c.groups[1] > 65535) return ATTN_ERR_INVALID_ARG;
+  const Cut c = cut(p.tokens, q.H + k.H, d, op, dtype == ATTN_DTYPE_BF16 ? 2 : 4);
+  if (c.grid_x < 0 || c.groups > 65535) return ATTN_ERR_INVALID_ARG;
   const RopeSide *in[2] = {&q, &k};
   for (int i = 0; i < 2; ++i) {
     const RopeSide &s = *in[i];
     Side &o = p.side[i];
     o = Side{s.x, s.dy, s.y, s.w, s.x_st.batch, s.x_st.head, s.x_st.token, s.y_st.batch, s.y_st.head,
-             s.y_st.token, s.dy_st.batch, s.dy_st.head, s.dy_st.token, s.dw, s.H, c.groups[i], c.per[i]};
+             s.y_st.token, s.dy_st.batch, s.dy_st.head, s.dy_st.token, s.H};
   }
   p.positions = positions;
   p.pos_stride = pos_stride;
   p.inv_freq = inv_freq;
   p.partial = static_cast<float *>(workspace);
   p.N = N;
+  p.per_group = c.per;
   p.rot = rot;
   p.factor = factor;
   p.sign = (transpose || bwd) ? -1.f : 1.f;
@@ -456,10 +549,10 @@ attn_status_t launch_rope(const RopeSide &q, const RopeSide &k, const int *posit
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const float *partial = p.partial;
-  const int rows0 = c.grid_x * c.groups[0], rows1 = c.grid_x * c.groups[1];
+  const int rows = c.grid_x * c.groups;
   const cudaError_t err =
-      d == 128 ? cudaLaunchKernelEx(&cfg, rope_dw_kernel<128>, partial, q.dw, k.dw, rows0, rows1)
-               : cudaLaunchKernelEx(&cfg, rope_dw_kernel<64>, partial, q.dw, k.dw, rows0, rows1);
+      d == 128 ? cudaLaunchKernelEx(&cfg, rope_dw_kernel<128>, partial, q.dw, k.dw, rows)
+               : cudaLaunchKernelEx(&cfg, rope_dw_kernel<64>, partial, q.dw, k.dw, rows);
   if (err != cudaSuccess) return ATTN_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
