@@ -14,13 +14,14 @@
 // whose new tokens hold a NaN or an infinity gets the scale NaN: the sequence's
 // attention then is NaN, as it would be over a 16-bit cache.
 //
-// Exact quotients without dividing: the product with inv = 1/s' (or s/s') is off
-// by at most a few parts in 2^24, so each element is rounded twice, from x * lo
-// and from x * hi with lo, hi = inv (1 -+ 2^-22), which enclose the quotient.
-// Rounding is monotonic: where both give one code, it is the quotient's.
-// Where they differ (a quotient within 2^-22 of a tie, a few in a million) the
-// lane divides in 64 bits, where code * s and the comparison with a tie are
-// exact.
+// Exact quotients: each product with 1 / s' is corrected by its remainder, whose
+// sign then decides the rounding (see codes8), for every element alike.  bf16
+// values meet ties often: x = amax / 2 is 63.5 steps of INT8 but for the scale's
+// own rounding, and every power of two times 3/4 amax may lie half way between
+// two E4M3 codes.  (Two products that enclose the quotient, and a division in 64
+// bits where they round apart, took 24 us (INT8) and 36 us (E4M3) for 16 chunks
+// of 512 tokens of 8 heads, d = 128; the remainder where they round apart as long
+// as the remainder everywhere, 17 and 18 us.)
 //
 // What bounds it: HBM for long chunks and for reading, one chain of dependent
 // loads (lengths, block table, data) for a decode step.  One warp takes one
@@ -50,54 +51,21 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 
 // Four floats to four codes (element 0 in the low byte), rounded to nearest
-// even.  E4M3 saturates at 448; INT8 takes |x * f| <= 127.5 - 2^-10 at most.
+// even.  E4M3 saturates at 448; INT8 takes |q| below 127.5.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes4(const float *x, float f) {
+__device__ __forceinline__ uint32_t codes4(const float *q) {
   if constexpr (FMT == ATTN_KV_E4M3) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * f), "f"(x[0] * f));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * f), "f"(x[2] * f));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[1]), "f"(q[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[3]), "f"(q[2]));
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
   } else {
-    // x * f + 1.5 * 2^23: the sum's unit is 1, so its low byte is the code.
+    // q + 1.5 * 2^23: the sum's unit is 1, so its low byte is the code.
     constexpr float kMagic = 12582912.f;
-    const uint32_t a = __float_as_uint(fmaf(x[0], f, kMagic)), b = __float_as_uint(fmaf(x[1], f, kMagic));
-    const uint32_t c = __float_as_uint(fmaf(x[2], f, kMagic)), d = __float_as_uint(fmaf(x[3], f, kMagic));
+    const uint32_t a = __float_as_uint(q[0] + kMagic), b = __float_as_uint(q[1] + kMagic);
+    const uint32_t c = __float_as_uint(q[2] + kMagic), d = __float_as_uint(q[3] + kMagic);
     return prmt(prmt(a, b, 0x0040u), prmt(c, d, 0x0040u), 0x5410u);
   }
-}
-
-// One code of x * num / den from the quotient in 64 bits.
-template <int FMT>
-__device__ __noinline__ uint32_t code_exact(float x, float num, float den) {
-  const double q = static_cast<double>(x) * static_cast<double>(num) / static_cast<double>(den);
-  if constexpr (FMT == ATTN_KV_E4M3) {
-    // To 24 bits toward zero with the lost part kept as a set last bit, so that
-    // the second rounding sees a tie only where there is one.
-    float f = __double2float_rz(q);
-    if (static_cast<double>(f) != q) f = __uint_as_float(__float_as_uint(f) | 1u);
-    uint16_t h;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.f), "f"(f));
-    return h & 0xffu;
-  } else {
-    return static_cast<uint32_t>(max(-127, min(127, __double2int_rn(q)))) & 0xffu;
-  }
-}
-
-// Eight floats to eight codes of x * num / den; lo and hi enclose num / den.
-template <int FMT>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float lo, float hi, float num, float den) {
-  uint2 c = make_uint2(codes4<FMT>(x, lo), codes4<FMT>(x + 4, lo));
-  const uint2 e = make_uint2(codes4<FMT>(x, hi), codes4<FMT>(x + 4, hi));
-  if (c.x != e.x || c.y != e.y) {
-    c = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c.x |= code_exact<FMT>(x[i], num, den) << (8 * i);
-      c.y |= code_exact<FMT>(x[4 + i], num, den) << (8 * i);
-    }
-  }
-  return c;
 }
 
 // Four codes to floats (exact).
@@ -121,6 +89,57 @@ __device__ __forceinline__ void values4(uint32_t w, float *v) {
     for (int i = 0; i < 4; ++i)
       v[i] = __uint_as_float(prmt(b, 0x4b000000u, 0x7440u | i)) - 8388736.f;
   }
+}
+
+// A division by den, scaled by a power of two so that den lies in [1, 2) and no
+// remainder that matters underflows.
+struct Divide {
+  float num, den, inv;  // num / den = the factor; inv = 1 / den
+  __device__ __forceinline__ Divide(float n, float d) {
+    const int e = static_cast<int>(__float_as_uint(d) >> 23) - 127;  // d: normal, positive
+    // 2^-e in two factors: e = 127 has no float of its own.
+    const float a = __uint_as_float(static_cast<uint32_t>(127 - (e >> 1)) << 23);
+    const float b = __uint_as_float(static_cast<uint32_t>(127 - (e - (e >> 1))) << 23);
+    num = n * a * b;
+    den = d * a * b;
+    inv = 1.f / den;
+  }
+};
+
+// Eight codes of x * num / den.  The quotient q of x' = x * num, its remainder r
+// and q1 = q + r * inv, which is within one unit of the exact quotient; the
+// remainder of q1 is exact, and its sign says on which side of q1 the quotient
+// lies.  Cut toward zero, with the last bit set where anything was cut, it then
+// rounds to the format as the exact quotient would: no value of the format and
+// none half way between two has that bit.  kPair: x' does not fit one float (a
+// code times a scale), and is taken as two.
+template <int FMT, bool kPair>
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divide &by) {
+  float q[8];
+  const float2 n2 = make_float2(by.num, by.num), i2 = make_float2(by.inv, by.inv);
+  const float2 d2 = make_float2(-by.den, -by.den), z2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 x2 = make_float2(x[i], x[i + 1]);
+    const float2 xp = fma2(x2, n2, z2);
+    const float2 xe = kPair ? fma2(x2, n2, make_float2(-xp.x, -xp.y)) : z2;
+    const float2 q0 = fma2(xp, i2, z2);
+    float2 r = fma2(q0, d2, xp);
+    if (kPair) r = add2(r, xe);
+    const float2 q1 = fma2(r, i2, q0);
+    float2 left = fma2(q1, d2, xp);
+    if (kPair) left = add2(left, xe);
+    const float l[2] = {left.x, left.y}, g[2] = {q1.x, q1.y};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t u = __float_as_uint(g[k]);
+      const bool some = l[k] != 0.f;
+      if (some && static_cast<int>(u ^ __float_as_uint(l[k])) < 0) --u;
+      if (some) u |= 1u;
+      q[i + k] = __uint_as_float(u);
+    }
+  }
+  return make_uint2(codes4<FMT>(q), codes4<FMT>(q + 4));
 }
 
 // The places of a sequence's chunk: new tokens ctx .. n-1, rows q0 .. of the
@@ -148,57 +167,68 @@ struct WriteParams {
   float *scales[2];
   const int *block_table, *seq_lens, *cu_q;
   unsigned *status;
-  int Hkv, T, max_q, max_blocks, num_pages, pages_per_seq;
+  int Hkv, T, max_q, max_blocks, num_pages, pages_per_seq, parts;
 };
 
-// Block: sequence and page of its chunk (x), four of the 2 * Hkv slices (y).
+// Block: sequence and page of its chunk, and four of the 2 * Hkv slices (K's heads,
+// then V's).
 template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 6) kv_write_kernel(const WriteParams p) {
   constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = kPage / RPP;  // lanes per row, rows per pass
   constexpr float kQmax = FMT == ATTN_KV_E4M3 ? 448.f : 127.f;
   const int lane = threadIdx.x & 31;
-  const int item = blockIdx.y * kWarps + (threadIdx.x >> 5);  // 2 * head + (0: K, 1: V)
-  const int s = blockIdx.x / p.pages_per_seq, j = blockIdx.x % p.pages_per_seq;
+  const int pages = gridDim.x / p.parts;
+  const int part = blockIdx.x / pages, at = blockIdx.x % pages;
+  const int s = at / p.pages_per_seq, j = at % p.pages_per_seq;
+  const int item = part * kWarps + (threadIdx.x >> 5);
   if (item >= 2 * p.Hkv) return;
   Chunk c;
   if (!chunk_of(p.seq_lens, p.cu_q, s, p.T, p.max_q, p.max_blocks, c)) {
-    if (threadIdx.x == 0 && j == 0 && blockIdx.y == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
+    if (threadIdx.x == 0 && j == 0 && part == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
     return;
   }
   const int page = c.ctx / kPage + j;
   if (c.nq == 0 || page * kPage >= c.n) return;
   const int pid = p.block_table[static_cast<size_t>(s) * p.max_blocks + page];
-  if (pid < 0 || pid >= p.num_pages) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
-    return;
-  }
   const int lo = max(c.ctx - page * kPage, 0), hi = min(kPage, c.n - page * kPage);
-  const int kv = item & 1, head = item >> 1;
+  const int kv = item >= p.Hkv, head = item - kv * p.Hkv;
   const int row = lane / LPR, col = (lane % LPR) * 8;
-  // Row r of the page is row q0 + page*16 + r - ctx of x.
+  // Row r of the page is row q0 + page*16 + r - ctx of x.  The new rows come
+  // along with the page's number, which they do not hang on.
   const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x[kv]) +
                            (c.q0 + static_cast<long long>(page) * kPage - c.ctx) * p.xt[kv] +
                            head * p.xh[kv] + col;
-  const size_t slice = static_cast<size_t>(pid) * p.Hkv + head;
-  uint8_t *codes = p.pages[kv] + slice * (kPage * D) + col;
-
-  uint4 in[PASSES];   // new rows
-  uint2 was[PASSES];  // earlier rows' codes
-  const float s_old = lo > 0 ? p.scales[kv][slice] : 0.f;
+  uint4 in[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int r = i * RPP + row;
     in[i] = make_uint4(0, 0, 0, 0);
     if (r >= lo && r < hi) in[i] = *reinterpret_cast<const uint4 *>(x + r * p.xt[kv]);
-    if (r < lo) was[i] = *reinterpret_cast<const uint2 *>(codes + r * D);
   }
-  // Largest magnitude as 15-bit patterns, two at a time: NaN above infinity
-  // above every finite value.
-  uint32_t top = 0;
+  if (pid < 0 || pid >= p.num_pages) {
+    if (threadIdx.x == 0 && part == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
+    return;
+  }
+  const size_t slice = static_cast<size_t>(pid) * p.Hkv + head;
+  uint8_t *codes = p.pages[kv] + slice * (kPage * D) + col;
+  uint2 was[PASSES];  // earlier rows' codes
+  const float s_old = lo > 0 ? p.scales[kv][slice] : 0.f;
+  if (lo > 0) {
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i)
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(in[i].x & 0x7fff7fffu, in[i].y & 0x7fff7fffu),
-                                 __vmaxu2(in[i].z & 0x7fff7fffu, in[i].w & 0x7fff7fffu)));
+    for (int i = 0; i < PASSES; ++i)
+      if (i * RPP + row < lo) was[i] = *reinterpret_cast<const uint2 *>(codes + (i * RPP + row) * D);
+  }
+  // Largest magnitude, two at a time, as bits: NaN above infinity above every
+  // finite value.
+  __nv_bfloat162 most = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      most = __hmax2_nan(most, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e])));
+  }
+  uint32_t top = *reinterpret_cast<const uint32_t *>(&most) & 0x7fff7fffu;
   top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
   float s_new = fmaxf(__uint_as_float(top << 16) / kQmax, 1.17549435e-38f);
   const bool odd = top >= 0x7f80u || !(fabsf(s_old) <= 3.4028235e38f);  // a NaN or infinity
@@ -206,15 +236,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const WriteParams
   if (odd) s_new = __uint_as_float(0x7fc00000u);
   if (lane == 0) p.scales[kv][slice] = s_new;
 
-  const float inv = 1.f / s_new;
-  const float inv_lo = inv * (1.f - 0x1p-22f), inv_hi = inv * (1.f + 0x1p-22f);
   const bool again = lo > 0 && s_new != s_old && !odd;
-  float ratio_lo = 0.f, ratio_hi = 0.f;
-  if (again) {
-    const float ratio = s_old / s_new;
-    ratio_lo = ratio * (1.f - 0x1p-22f);
-    ratio_hi = ratio * (1.f + 0x1p-22f);
-  }
+  const Divide by(1.f, odd ? 1.f : s_new), rescale(again ? s_old : 0.f, odd ? 1.f : s_new);
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int r = i * RPP + row;
@@ -227,11 +250,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv_write_kernel(const WriteParams
         v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
       }
       *reinterpret_cast<uint2 *>(codes + r * D) =
-          odd ? make_uint2(0, 0) : codes8<FMT>(v, inv_lo, inv_hi, 1.f, s_new);
+          odd ? make_uint2(0, 0) : codes8<FMT, false>(v, by);
     } else if (r < lo && again) {
       values4<FMT>(was[i].x, v);
       values4<FMT>(was[i].y, v + 4);
-      *reinterpret_cast<uint2 *>(codes + r * D) = codes8<FMT>(v, ratio_lo, ratio_hi, s_old, s_new);
+      *reinterpret_cast<uint2 *>(codes + r * D) = codes8<FMT, true>(v, rescale);
     }
   }
 }
@@ -242,31 +265,33 @@ struct ReadParams {
   void *out[2];  // [T, Hkv, D]
   const int *block_table, *seq_lens, *cu_q;
   unsigned *status;
-  int Hkv, T, max_q, max_blocks, num_pages, pages_per_seq;
+  int Hkv, T, max_q, max_blocks, num_pages, pages_per_seq, parts;
 };
 
 __device__ __forceinline__ void store4(float *p, const float *v) {
   *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// Block: sequence and page of its range (x), four K/V heads (y).
+// Block: sequence and page of its range, and four K/V heads.
 template <int D, int FMT, typename T>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadParams p) {
   constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = kPage / RPP;
   const int lane = threadIdx.x & 31;
-  const int head = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int s = blockIdx.x / p.pages_per_seq, j = blockIdx.x % p.pages_per_seq;
+  const int part = blockIdx.x % p.parts;
+  const int at = blockIdx.x / p.parts;
+  const int s = at / p.pages_per_seq, j = at % p.pages_per_seq;
+  const int head = part * kWarps + (threadIdx.x >> 5);
   if (head >= p.Hkv) return;
   Chunk c;
   if (!chunk_of(p.seq_lens, p.cu_q, s, p.T, p.max_q, p.max_blocks, c)) {
-    if (threadIdx.x == 0 && j == 0 && blockIdx.y == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
+    if (threadIdx.x == 0 && j == 0 && part == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
     return;
   }
   const int page = c.ctx / kPage + j;
   if (c.nq == 0 || page * kPage >= c.n) return;
   const int pid = p.block_table[static_cast<size_t>(s) * p.max_blocks + page];
   const bool bad = pid < 0 || pid >= p.num_pages;
-  if (bad && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
+  if (bad && threadIdx.x == 0 && part == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
   const int lo = max(c.ctx - page * kPage, 0), hi = min(kPage, c.n - page * kPage);
   const int row = lane / LPR, col = (lane % LPR) * 8;
   const size_t slice = static_cast<size_t>(bad ? 0 : pid) * p.Hkv + head;
@@ -342,10 +367,11 @@ attn_status_t launch_kv_write_q8(const void *k, const void *v, const long long (
   p.max_blocks = max_blocks;
   p.num_pages = num_pages;
   p.pages_per_seq = static_cast<int>(pages_touched(max_q, max_blocks));
-  const long long gx = static_cast<long long>(S) * p.pages_per_seq;
-  const long long gy = (2LL * Hkv + kWarps - 1) / kWarps;
-  if (gx > 0x7fffffffLL || gy > 65535) return ATTN_ERR_INVALID_ARG;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  const long long parts = (2LL * Hkv + kWarps - 1) / kWarps;
+  const long long blocks = static_cast<long long>(S) * p.pages_per_seq;
+  if (blocks > 0x7fffffffLL / parts) return ATTN_ERR_INVALID_ARG;
+  p.parts = static_cast<int>(parts);
+  const dim3 grid(static_cast<unsigned>(blocks * parts));
   if (d == 128) {
     if (kv_format == ATTN_KV_E4M3) kv_write_kernel<128, ATTN_KV_E4M3><<<grid, kWarps * 32, 0, stream>>>(p);
     else kv_write_kernel<128, ATTN_KV_INT8><<<grid, kWarps * 32, 0, stream>>>(p);
@@ -384,10 +410,11 @@ attn_status_t launch_kv_read_q8(const void *k_pages, const void *v_pages, const 
   p.max_blocks = max_blocks;
   p.num_pages = num_pages;
   p.pages_per_seq = static_cast<int>(pages_touched(max_q, max_blocks));
-  const long long gx = static_cast<long long>(S) * p.pages_per_seq;
-  const long long gy = (static_cast<long long>(Hkv) + kWarps - 1) / kWarps;
-  if (gx > 0x7fffffffLL || gy > 65535) return ATTN_ERR_INVALID_ARG;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  const long long parts = (static_cast<long long>(Hkv) + kWarps - 1) / kWarps;
+  const long long blocks = static_cast<long long>(S) * p.pages_per_seq;
+  if (blocks > 0x7fffffffLL / parts) return ATTN_ERR_INVALID_ARG;
+  p.parts = static_cast<int>(parts);
+  const dim3 grid(static_cast<unsigned>(blocks * parts));
   if (d == 128) {
     if (kv_format == ATTN_KV_E4M3) launch_read<128, ATTN_KV_E4M3>(p, dtype, grid, stream);
     else launch_read<128, ATTN_KV_INT8>(p, dtype, grid, stream);
