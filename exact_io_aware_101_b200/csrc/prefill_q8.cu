@@ -60,7 +60,7 @@ constexpr int BN = 128;  // keys of a tile
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = BN / kPage;
 constexpr int NUM_THREADS = 512;
-constexpr int kRegsMma = 72, kRegsWiden = 72, kRegsSoft = 184;
+constexpr int kRegsMma = 88, kRegsWiden = 104, kRegsSoft = 160;
 static_assert(128 * (kRegsMma + kRegsWiden + 2 * kRegsSoft) <= NUM_THREADS * 128,
               "setmaxnreg split must fit the block's launch registers");
 constexpr int kRankMax = NUM_THREADS;   // sequences ranked by length
@@ -92,7 +92,9 @@ struct Shared {
   uint64_t empty[8];
   uint64_t q_full[2];
   uint64_t s_full[2];
+  uint64_t p_half[2];
   uint64_t p_full[2];
+  uint64_t o_half[2];
   uint64_t o_full[2];
   uint64_t mma_done;
   alignas(16) float k_scale[kScaleRing][kPagesPerTile];
@@ -167,29 +169,17 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &a, uint32_t &b) {
   }
 }
 
-// A thread's whole score row, in two loads (ptxas holds one instruction's
-// registers to the launch's 128 a thread).
-__device__ __forceinline__ void load_row(uint32_t addr, uint32_t (&sv)[128]) {
-  tmem_ld64(addr, *reinterpret_cast<uint32_t(*)[64]>(sv));
-  tmem_ld64(addr + 64, *reinterpret_cast<uint32_t(*)[64]>(sv + 64));
-}
-__device__ __forceinline__ void row_loaded(uint32_t (&sv)[128]) {
-  tmem_ld_wait64(*reinterpret_cast<uint32_t(*)[64]>(sv));
-  tmem_ld_wait64(*reinterpret_cast<uint32_t(*)[64]>(sv + 64));
-}
-
-// 32 columns cc*32 .. of one thread's score row -> 16 f16 pairs of P = 2^(s*c -
-// m), c the multiplier of the columns' page, and their part of the row sum.
-__device__ __forceinline__ void exp_chunk(const uint32_t (&sv)[128], int cc, float c0, float c1,
-                                          float m, uint32_t *pk, float2 &sum_a, float2 &sum_b) {
+// Half a score row (64 columns, four pages) -> 32 f16 pairs of P = 2^(s*c - m), c
+// the multiplier of the columns' page; returns the part of the row sum.
+__device__ __forceinline__ float exp_half(const uint32_t (&sv)[64], const float *c, float m,
+                                          uint32_t (&pk)[32]) {
   const float2 nm2 = make_float2(-m, -m);
+  float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
-    const int col = cc * 32 + i;
-    const float c = i < 16 ? c0 : c1;
-    const float2 c2 = make_float2(c, c);
-    const float2 x0 = fma2(make_float2(__uint_as_float(sv[col]), __uint_as_float(sv[col + 1])), c2, nm2);
-    const float2 x1 = fma2(make_float2(__uint_as_float(sv[col + 2]), __uint_as_float(sv[col + 3])), c2, nm2);
+  for (int i = 0; i < 64; i += 4) {
+    const float2 c2 = make_float2(c[i / kPage], c[i / kPage]);
+    const float2 x0 = fma2(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), c2, nm2);
+    const float2 x1 = fma2(make_float2(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), c2, nm2);
     const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
     const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
     sum_a = add2(sum_a, p0);
@@ -197,6 +187,10 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&sv)[128], int cc, flo
     pk[i >> 1] = pack_f16x2(p0.x, p0.y);
     pk[(i >> 1) + 1] = pack_f16x2(p1.x, p1.y);
   }
+  return (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
+}
+__device__ __forceinline__ void store_half(uint32_t addr, const uint32_t (&pk)[32]) {
+  tmem_st32(addr, pk);
 }
 
 // A sequence's chunk: rows q0 .. q0 + nq - 1, its last token the n-th.  False
@@ -298,7 +292,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh->q_full[t], BM);
       mbar_init(&sh->s_full[t], 1);
+      mbar_init(&sh->p_half[t], BM);
       mbar_init(&sh->p_full[t], BM);
+      mbar_init(&sh->o_half[t], 1);
       mbar_init(&sh->o_full[t], 1);
     }
     mbar_init(&sh->mma_done, 1);
@@ -384,14 +380,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         }
         if (one) tc_commit(&sh->s_full[t]);
       };
-      auto issue_pv = [&](int t, int vidx, bool acc) {  // O_t (+)= P_t V
+      // O_t (+)= P_t V, in halves of 64 keys as their P comes; st: step of the tile.
+      auto issue_pv = [&](int t, int vidx, int st) {
         const uint64_t vd = vdesc0 + ((slot_of(vidx) * C::TILE_BYTES) >> 4);
+        if (!mbar_wait(&sh->p_half[t], st & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
+        for (int ks = 0; ks < BN / 32; ++ks)
           if (one)
             mma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4),
-                   C::IDESC_PV, (acc || ks > 0) ? 1u : 0u);
+                   C::IDESC_PV, (st > 0 || ks > 0) ? 1u : 0u);
+        if (one) tc_commit(&sh->o_half[t]);
+        if (!mbar_wait(&sh->p_full[t], st & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = BN / 32; ks < BN / 16; ++ks)
+          if (one)
+            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + ks * 8, vd + ((ks * 16 * 128) >> 4),
+                   C::IDESC_PV, 1u);
         if (one) tc_commit(&sh->o_full[t]);
+        return true;
       };
       // Tile j sits at ring index 2 * (j - jlo) (K) and one behind (V).
       auto has = [&](int t, int j) {
@@ -411,19 +419,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         const bool more = j + 1 < jhi;
         if (!(ok = wait_full(2 * rj + 1))) break;
         if (more && !(ok = wait_full(2 * rj + 2))) break;
-        if (has(0, j)) {
-          if (!(ok = mbar_wait(&sh->p_full[0], (j - js0) & 1, abort_flag, p.status))) break;
-          tc_fence_after();
-          issue_pv(0, 2 * rj + 1, j > js0);
-        }
+        if (has(0, j) && !(ok = issue_pv(0, 2 * rj + 1, j - js0))) break;
         // P_t(j) lies over S_t: the MMAs of one thread run in order, so S_t(j+1)
         // is written only after P_t(j) has been read.
         if (more && has(0, j + 1)) issue_s(0, 2 * rj + 2);
-        if (has(1, j)) {
-          if (!(ok = mbar_wait(&sh->p_full[1], (j - js1) & 1, abort_flag, p.status))) break;
-          tc_fence_after();
-          issue_pv(1, 2 * rj + 1, j > js1);
-        }
+        if (has(1, j) && !(ok = issue_pv(1, 2 * rj + 1, j - js1))) break;
         if (one) tc_commit(&sh->empty[slot_of(2 * rj + 1)]);
         if (more && has(1, j + 1)) issue_s(1, 2 * rj + 2);
         if (more && one) tc_commit(&sh->empty[slot_of(2 * rj + 2)]);
@@ -640,6 +640,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       mbar_arrive(&sh->q_full[t]);
     }
     const float slope2 = kAlibi && valid ? p.slopes[hq] * 1.4426950408889634f : 0.f;
+    // A warp without a row of its own (a chunk of a few tokens) only hands on.
+    const bool idle = !__any_sync(0xffffffffu, valid);
     float m = -INFINITY;  // reference max, in log2 units of scaled scores
     float l = 0.f;
     bool ok = true;
@@ -654,9 +656,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       ok = mbar_wait(&sh->s_full[t], jj & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      if (idle) {
+        mbar_arrive(&sh->p_half[t]);
+        mbar_arrive(&sh->p_full[t]);
+        continue;
+      }
       tc_fence_after();
-      uint32_t sv[128];
-      load_row(s_addr, sv);
+      // The multipliers of each page's columns.
       float cp[kPagesPerTile];
       {
         const float4 *ks = reinterpret_cast<const float4 *>(sh->k_scale[(j - jlo) % kScaleRing]);
@@ -664,92 +670,111 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         cp[0] = a.x * c_row; cp[1] = a.y * c_row; cp[2] = a.z * c_row; cp[3] = a.w * c_row;
         cp[4] = b.x * c_row; cp[5] = b.y * c_row; cp[6] = b.z * c_row; cp[7] = b.w * c_row;
       }
-      row_loaded(sv);
-      // An unmasked tile first takes P against the running reference as it
-      // stands, without looking for its own max.  Where every row's P sums to
-      // at most 255, each term is below 2^8 and the max-first step below would
-      // have kept the reference too.  Otherwise the S row, which the attempt
-      // left untouched in TMEM, is read again and the tile goes max first.
-      bool fast = false, missed = false;
+      // The row goes in halves of 64 columns, and the first half's P is handed
+      // on while the second is worked on.  P of columns 0-63 lies over S columns
+      // 0-31, that of 64-127 over 32-63.
+      uint32_t sv[64], pk[32];
+      bool first_done = false;  // the first half's P is out, against m as it was
       if (attempt) {
-        uint32_t pk[64];
-        float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc)
-          exp_chunk(sv, cc, cp[2 * cc], cp[2 * cc + 1], m, pk + cc * 16, sum_a, sum_b);
-        const float l_tile = (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
-        missed = !(l_tile <= 255.0f);
-        fast = !__any_sync(0xffffffffu, missed);
-        if (fast) {
-          l += l_tile;
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc)
-            tmem_st16(s_addr + cc * 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + cc * 16));
-          // The scores are dead on this path: no copy need stay across it.
-#pragma unroll
-          for (int i = 0; i < 128; ++i) asm("" : "=r"(sv[i]));
-        } else {
-          load_row(s_addr, sv);
-          row_loaded(sv);
-        }
-      }
-      if (!fast) {
-        // To scaled scores (log2 units) with the bias; masked ones to -inf,
-        // whatever they were.
-        const float rb = kAlibi ? slope2 * static_cast<float>(j * BN - (ck.ctx + tok)) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 128; ++i) {
-          float x = __uint_as_float(sv[i]) * cp[i / kPage];
-          if (kAlibi) x += fmaf(slope2, static_cast<float>(i), rb);
-          sv[i] = __float_as_uint(x);
-        }
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i < lo || i >= hi) sv[i] = 0xff800000u;
-        }
-        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 128; i += 8) {
-          m0 = fmax3(m0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-          m1 = fmax3(m1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
-          m2 = fmax3(m2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
-          m3 = fmax3(m3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
-        }
-        const float m_new = fmaxf(m, fmax3(m0, m1, fmaxf(m2, m3)));
-        const bool resc = m_new > m + 8.0f || (missed && m_new > m);
-        const float alpha = resc ? ex2(m - m_new) : 1.0f;
-        if (resc) m = m_new;
-        l *= alpha;
-        // A row that has seen no visible key yet keeps m = -inf; its masked
-        // scores must still give P = 0, not -inf - (-inf).
-        const float m_use = (m == -INFINITY) ? 0.f : m;
-        float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t pk[16];
-          exp_chunk(sv, cc, 1.f, 1.f, m_use, pk, sum_a, sum_b);
-          tmem_st16(s_addr + cc * 16, pk);
-        }
-        l += (sum_a.x + sum_a.y) + (sum_b.x + sum_b.y);
-        if (jj > 0 && __any_sync(0xffffffffu, resc)) {
-          // Lazy rescale of O.  O is stable here: this tile's S completing
-          // implies the previous PV completed, and this tile's PV waits for
-          // p_full.
-#pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t ov[32];
-            tmem_ld32(o_addr + cc * 32, ov);
-            tmem_ld_wait(ov);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-            tmem_st32(o_addr + cc * 32, ov);
+        // An unmasked tile first takes P against the running reference as it
+        // stands, without looking for its own max.  Where a half's sum is at
+        // most 255 in every row, each of its terms is below 2^8 and the
+        // max-first step below would have kept the reference too.
+        tmem_ld64(s_addr, sv);
+        tmem_ld_wait64(sv);
+        const float l0 = exp_half(sv, cp, m, pk);
+        if (__all_sync(0xffffffffu, l0 <= 255.0f)) {
+          first_done = true;
+          tmem_ld64(s_addr + 64, sv);
+          store_half(s_addr, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&sh->p_half[t]);
+          l += l0;
+          tmem_ld_wait64(sv);
+          const float l1 = exp_half(sv, cp + 4, m, pk);
+          if (__all_sync(0xffffffffu, l1 <= 255.0f)) {
+            l += l1;
+            store_half(s_addr + 32, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&sh->p_full[t]);
+            continue;
           }
         }
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&sh->p_full[t]);
+      // Max first, over what is not out yet.
+      // To scaled scores (log2 units) with the bias; masked ones to -inf,
+      // whatever they were.
+      const float rb = kAlibi ? slope2 * static_cast<float>(j * BN - (ck.ctx + tok)) : 0.f;
+      auto scaled_half = [&](int h) {
+        tmem_ld64(s_addr + 64 * h, sv);
+        tmem_ld_wait64(sv);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          float x = __uint_as_float(sv[i]) * (h ? cp[4 + i / kPage] : cp[i / kPage]);
+          if (kAlibi) x += fmaf(slope2, static_cast<float>(64 * h + i), rb);
+          sv[i] = __float_as_uint(x);
+        }
+        if (masked) {
+          const int lo_h = lo - 64 * h, hi_h = hi - 64 * h;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < lo_h || i >= hi_h) sv[i] = 0xff800000u;
+        }
+      };
+      auto half_max = [&]() {
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          m0 = fmax3(m0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+          m1 = fmax3(m1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
+        }
+        return fmaxf(m0, m1);
+      };
+      float m_new = m;
+#pragma unroll 1
+      for (int h = first_done; h < 2; ++h) {
+        scaled_half(h);
+        m_new = fmaxf(m_new, half_max());
+      }
+      // The reference moves where it must (by 2^8 or more), and after a miss.
+      const bool resc = m_new > m + 8.0f || (attempt && m_new > m);
+      const float alpha = resc ? ex2(m - m_new) : 1.0f;
+      if (resc) m = m_new;
+      l *= alpha;
+      if (jj > 0 && __any_sync(0xffffffffu, resc)) {
+        // Lazy rescale of O.  S(j) being there implies that PV(j-1) is done; of
+        // PV(j), the first half may be under way if its P is out.
+        if (first_done) {
+          ok = mbar_wait(&sh->o_half[t], jj & 1, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t ov[32];
+          tmem_ld32(o_addr + cc * 32, ov);
+          tmem_ld_wait(ov);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+          tmem_st32(o_addr + cc * 32, ov);
+        }
+      }
+      // A row that has seen no visible key yet keeps m = -inf; its masked scores
+      // must still give P = 0, not -inf - (-inf).
+      const float m_use = (m == -INFINITY) ? 0.f : m;
+      const float ones[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll 1
+      for (int h = first_done; h < 2; ++h) {
+        scaled_half(h);
+        l += exp_half(sv, ones, m_use, pk);
+        store_half(s_addr + 32 * h, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(h ? &sh->p_full[t] : &sh->p_half[t]);
+      }
     }
     if (ok && nt > 0) {
       ok = mbar_wait(&sh->o_full[t], (nt - 1) & 1, abort_flag, p.status);
