@@ -72,9 +72,9 @@ constexpr int kEdge = 4;       // tiles that a row may see in part, at either en
 template <int D>
 struct Cfg {
   static constexpr int TILE_BYTES = BM * D * 2;  // a Q, K or V tile in f16
-  static constexpr int NST = (D == 64) ? 8 : 4;  // ring slots
+  static constexpr int NST = (D == 64) ? 6 : 3;  // ring slots
   static constexpr int RAW_BYTES = BN * D;       // a K or V tile in codes
-  static constexpr int NRAW = (D == 64) ? 4 : 2; // raw slots: K and V in turn
+  static constexpr int NRAW = 4;                 // raw slots
   static constexpr int RING_OFF = 2 * TILE_BYTES;
   static constexpr int RAW_OFF = RING_OFF + NST * TILE_BYTES;
   static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW_BYTES;
@@ -96,6 +96,7 @@ struct Shared {
   uint64_t p_full[2];
   uint64_t o_half[2];
   uint64_t o_full[2];
+  uint64_t mrg_full;  // twin: tile 1's m and l are published
   uint64_t mma_done;
   alignas(16) float k_scale[kScaleRing][kPagesPerTile];
   alignas(16) float v_scale[kScaleRing][kPagesPerTile];
@@ -114,14 +115,19 @@ struct Params {
   const int *block_table, *seq_lens, *cu_q;
   __nv_bfloat16 *o;
   float *lse;
-  float *o_part, *l2_part;  // nsplit > 1: [T][Hq][nsplit][D] and [T][Hq][nsplit]
+  // Split over keys (split): each sequence's first CTA and its parts per work
+  // item, [2][S]; and every CTA's rows, normalised, with their log2-sum-exps,
+  // [CTA][rows_cap][D] and [CTA][rows_cap].
+  int *plan;
+  float *o_part, *l2_part;
   const float *slopes;
   unsigned *status;
   int S, Hq, Hkv, T, max_q, max_blocks, num_pages;
   int heads;      // query heads per CTA (rows of a token)
   int tokens;     // tokens per tile: floor(128 / heads)
-  int pairs;      // tile pairs for max_q tokens
-  int nsplit;
+  int span;       // tokens of a CTA: those of two tiles, or of one (twin)
+  int pairs;      // CTAs for max_q tokens
+  int split, rows_cap;
   float scale_log2;
   int window;
 };
@@ -209,7 +215,104 @@ __device__ __forceinline__ bool chunk_of(const Params &p, int s, Chunk &c) {
          c.n <= static_cast<long long>(p.max_blocks) * kPage;
 }
 
-template <int D, int FMT, bool kAlibi>
+// The work item of a CTA of a split call: at most kSMs CTAs share the work items'
+// key tiles, an item of `tiles` tiles in ceil(tiles / c) parts with the smallest c
+// (found from below) that needs no more CTAs.  Every warp works it out alike.
+struct Item {
+  int seq, pair, group, part, parts, first;  // first: the sequence's first CTA
+};
+__device__ __forceinline__ bool plan_of(const Params &p, int cta, int lane, Item &it) {
+  constexpr int kMost = (kSMs + 31) / 32;  // a split call has fewer sequences than SMs
+  constexpr int kFewest = 4;               // tiles worth a part of its own
+  const int groups = p.Hq / p.heads;
+  int items[kMost], tiles[kMost];
+  int total = 0;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int s = k * 32 + lane;
+    items[k] = 0;
+    tiles[k] = 1;
+    if (s < p.S) {
+      Chunk c;
+      if (!chunk_of(p, s, c)) {
+        items[k] = 1;  // (to say so)
+      } else if (c.nq > 0) {
+        items[k] = (c.nq + p.span - 1) / p.span * groups;
+        tiles[k] = (c.n + BN - 1) / BN;
+        if (p.window > 0) tiles[k] = min(tiles[k], (min(p.window, c.n) + p.span) / BN + 2);
+      }
+    }
+    total += items[k] * tiles[k];
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  int c = max(kFewest, (total + kSMs - 1) / kSMs);
+  while (true) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kMost; ++k) n += items[k] * ((tiles[k] + c - 1) / c);
+    if (__reduce_add_sync(0xffffffffu, n) <= kSMs) break;
+    c += max(1, c >> 4);  // (ends: one part an item is no more than kSMs CTAs)
+  }
+  int before = 0;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    const int parts = (tiles[k] + c - 1) / c, mine = items[k] * parts;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, cta < before + upto);
+    if (here) {
+      const int src = __ffs(here) - 1;
+      it.seq = k * 32 + src;
+      it.parts = __shfl_sync(0xffffffffu, parts, src);
+      it.first = before + __shfl_sync(0xffffffffu, upto - mine, src);
+      const int at = cta - it.first, item = at / it.parts;
+      it.part = at - item * it.parts;
+      it.pair = item / groups;
+      it.group = item - it.pair * groups;
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
+}
+
+// Entry i of the order in which a CTA's `total` K and V tiles (of total / 2 key
+// tiles from jlo on) go through the rings: its tensor, key tile and the slot of its
+// page scales.  Two row tiles share every key tile: K(s) V(s) in turn.  Twin tiles,
+// which hold the same rows, each walk half of the key tiles (n0, and n1 = n0 or
+// n0 - 1): K0(0) K1(0), then V0(s) K0(s+1) V1(s) K1(s+1) without those past the ends.
+template <bool kTwin>
+__device__ __forceinline__ void entry(int i, int jlo, int total, bool &v, int &j, int &slot) {
+  int t = 0, s = i >> 1;
+  v = i & 1;
+  if (kTwin) {
+    const int n = total >> 1, n0 = (n + 1) >> 1;
+    if (i == total - 1) {  // the last V: of tile 1 where the halves are equal
+      t = (n & 1) ^ 1;
+      s = n0 - 1;
+      v = true;
+    } else if (i < 2) {
+      t = i;
+      s = 0;
+      v = false;
+    } else {
+      t = ((i - 2) >> 1) & 1;
+      v = (i & 1) == 0;
+      s = ((i - 2) >> 2) + (v ? 0 : 1);
+    }
+    j = jlo + (t ? n0 : 0) + s;
+    slot = (2 * s + t) % kScaleRing;
+  } else {
+    j = jlo + s;
+    slot = s % kScaleRing;
+  }
+}
+
+template <int D, int FMT, bool kAlibi, bool kTwin>
 __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params p) {
   using C = Cfg<D>;
   grid_dependents_launch();  // the joining kernel may be scheduled behind this grid
@@ -221,63 +324,83 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
   volatile int *abort_flag = &sh->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- work item: longest sequence first, its last (heaviest) pair first,
-  // so that the last wave holds the short ones.  Past kRankMax sequences the
-  // order stays as given.
+  // ---- work item.  A split call's by its plan; else the longest sequence first,
+  // its last (heaviest) pair first, so that the last wave holds the short ones.
+  // Past kRankMax sequences the order stays as given.
   const int groups = p.Hq / p.heads;  // head groups of a token
-  const int per_pair = groups * p.nsplit;
-  const int per_seq = p.pairs * per_pair;
   const int lin = static_cast<int>(blockIdx.x);
-  const int rank_of = lin / per_seq, rem = lin - rank_of * per_seq;
-  const int pair = p.pairs - 1 - rem / per_pair;
-  const int group = (rem % per_pair) / p.nsplit, part = rem % p.nsplit;
-  int seq = rank_of;
-  if (p.S > 1 && p.S <= kRankMax) {
-    int *s_len = reinterpret_cast<int *>(smem);  // (where the queries come later)
-    int &s_seq = s_len[kRankMax];
-    const int t = static_cast<int>(threadIdx.x);
-    if (t < p.S) s_len[t] = p.seq_lens[t];
-    __syncthreads();
-    if (t < p.S) {
-      const int nt = s_len[t];
-      int rank = 0;
-      for (int u = 0; u < p.S; ++u) rank += (s_len[u] > nt) || (s_len[u] == nt && u < t);
-      if (rank == rank_of) s_seq = t;
+  int seq, pair, group, part = 0, parts = 1;
+  if (p.split) {
+    Item it;
+    if (!plan_of(p, lin, lane, it)) return;
+    seq = it.seq;
+    pair = it.pair;
+    group = it.group;
+    part = it.part;
+    parts = it.parts;
+    if (lin == it.first && threadIdx.x == 0) {
+      p.plan[seq] = it.first;
+      p.plan[p.S + seq] = it.parts;
     }
-    __syncthreads();
-    seq = s_seq;
-    __syncthreads();
+  } else {
+    const int per_seq = p.pairs * groups;
+    const int rank_of = lin / per_seq, rem = lin - rank_of * per_seq;
+    pair = p.pairs - 1 - rem / groups;
+    group = rem % groups;
+    seq = rank_of;
+    if (p.S > 1 && p.S <= kRankMax) {
+      int *s_len = reinterpret_cast<int *>(smem);  // (where the queries come later)
+      int &s_seq = s_len[kRankMax];
+      const int t = static_cast<int>(threadIdx.x);
+      if (t < p.S) s_len[t] = p.seq_lens[t];
+      __syncthreads();
+      if (t < p.S) {
+        const int nt = s_len[t];
+        int rank = 0;
+        for (int u = 0; u < p.S; ++u) rank += (s_len[u] > nt) || (s_len[u] == nt && u < t);
+        if (rank == rank_of) s_seq = t;
+      }
+      __syncthreads();
+      seq = s_seq;
+      __syncthreads();
+    }
   }
   Chunk ck;
   if (!chunk_of(p, seq, ck)) {
     if (threadIdx.x == 0 && pair == 0 && group == 0 && part == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
     return;
   }
-  const int tok0 = pair * 2 * p.tokens;  // first token of tile 0
+  const int tok0 = pair * p.span;  // first token of tile 0 (and, twin, of tile 1)
   if (tok0 >= ck.nq) return;
-  const int h0 = group * p.heads;                  // first query head
+  const int h0 = group * p.heads;                            // first query head
   const int hkv = h0 / (p.Hq / p.Hkv);
-  const bool rows1 = tok0 + p.tokens < ck.nq;      // tile 1 has rows
+  const bool rows1 = !kTwin && tok0 + p.tokens < ck.nq;      // tile 1 has rows of its own
   // Key tiles [js_t, je_t) of each row tile.
   int je0 = (ck.ctx + min(tok0 + p.tokens, ck.nq) - 1) / BN + 1;
   int je1 = rows1 ? (ck.ctx + min(tok0 + 2 * p.tokens, ck.nq) - 1) / BN + 1 : 0;
   int js0 = p.window > 0 ? max(0, ck.ctx + tok0 - p.window + 1) / BN : 0;
   int js1 = p.window > 0 && rows1 ? max(0, ck.ctx + tok0 + p.tokens - p.window + 1) / BN : 0;
-  // Tiles from edge_hi on, and (with a window) those before edge_lo, hold keys
-  // that some row of this CTA does not see.  At most kEdge of each: the rows
+  // Tiles from edge_hi on, and (with a window) the first few from edge_0, hold
+  // keys that some row of this CTA does not see.  At most kEdge of each: the rows
   // span at most 256 positions.
   const int edge_hi = (ck.ctx + tok0 + 1) / BN;
   const int edge_0 = js0;
   int jlo = js0, jhi = max(je0, je1);
-  if (p.nsplit > 1) {  // this CTA's part of them
+  if (parts > 1) {  // this CTA's part of them
     const int n = jhi - jlo, first = jlo;
-    jlo = first + static_cast<int>(static_cast<long long>(n) * part / p.nsplit);
-    jhi = first + static_cast<int>(static_cast<long long>(n) * (part + 1) / p.nsplit);
+    jlo = first + static_cast<int>(static_cast<long long>(n) * part / parts);
+    jhi = first + static_cast<int>(static_cast<long long>(n) * (part + 1) / parts);
     js0 = max(js0, jlo);
     js1 = max(js1, jlo);
     je0 = min(je0, jhi);
     je1 = min(je1, jhi);
   }
+  if (kTwin) {
+    js0 = jlo;
+    je0 = js1 = jlo + (jhi - jlo + 1) / 2;
+    je1 = jhi;
+  }
+  const int total = 2 * (jhi - jlo);  // K and V tiles of the walk
 
   // ---- every page of those tiles must be in the pool; and their largest V scale.
   if (threadIdx.x == 0) {
@@ -297,6 +420,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       mbar_init(&sh->o_half[t], 1);
       mbar_init(&sh->o_full[t], 1);
     }
+    mbar_init(&sh->mrg_full, BM);
     mbar_init(&sh->mma_done, 1);
     sh->abort_flag = 0;
     sh->any_bad = 0;
@@ -325,16 +449,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       const bool none = jlo >= jhi;
       if (!none && threadIdx.x == 0) atomicOr(p.status, ATTN_DEV_BAD_PAGE);
       const float fill = none ? 0.f : NAN;
-      const int ntok = min(2 * p.tokens, ck.nq - tok0);
+      const int ntok = min(p.span, ck.nq - tok0);
       for (int i = threadIdx.x; i < ntok * p.heads * D; i += NUM_THREADS) {
         const int c = i % D, r = i / D;
-        const size_t row = static_cast<size_t>(ck.q0 + tok0 + r / p.heads) * p.Hq + h0 + r % p.heads;
-        if (p.nsplit == 1) {
+        if (!p.split) {
+          const size_t row = static_cast<size_t>(ck.q0 + tok0 + r / p.heads) * p.Hq + h0 + r % p.heads;
           p.o[row * D + c] = __float2bfloat16_rn(fill);
           if (c == 0) p.lse[row] = fill;
         } else {
-          p.o_part[(row * p.nsplit + part) * D + c] = fill;
-          if (c == 0) p.l2_part[row * p.nsplit + part] = none ? -INFINITY : fill;
+          const size_t row = static_cast<size_t>(lin) * p.rows_cap + r;
+          p.o_part[row * D + c] = fill;
+          if (c == 0) p.l2_part[row] = none ? -INFINITY : fill;
         }
       }
       return;
@@ -401,59 +526,114 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         if (one) tc_commit(&sh->o_full[t]);
         return true;
       };
-      // Tile j sits at ring index 2 * (j - jlo) (K) and one behind (V).
-      auto has = [&](int t, int j) {
-        return t == 0 ? (j >= js0 && j < je0) : (j >= js1 && j < je1);
-      };
       bool ok = wait_full(0);
       if (ok && js0 < je0) ok = mbar_wait(&sh->q_full[0], 0, abort_flag, p.status);
       if (ok && js1 < je1) ok = mbar_wait(&sh->q_full[1], 0, abort_flag, p.status);
-      if (ok) {
-        tc_fence_after();
-        if (has(0, jlo)) issue_s(0, 0);
-        if (has(1, jlo)) issue_s(1, 0);
-        if (one) tc_commit(&sh->empty[slot_of(0)]);
-      }
-      for (int rj = 0; ok && rj < jhi - jlo; ++rj) {
-        const int j = jlo + rj;
-        const bool more = j + 1 < jhi;
-        if (!(ok = wait_full(2 * rj + 1))) break;
-        if (more && !(ok = wait_full(2 * rj + 2))) break;
-        if (has(0, j) && !(ok = issue_pv(0, 2 * rj + 1, j - js0))) break;
-        // P_t(j) lies over S_t: the MMAs of one thread run in order, so S_t(j+1)
-        // is written only after P_t(j) has been read.
-        if (more && has(0, j + 1)) issue_s(0, 2 * rj + 2);
-        if (has(1, j) && !(ok = issue_pv(1, 2 * rj + 1, j - js1))) break;
-        if (one) tc_commit(&sh->empty[slot_of(2 * rj + 1)]);
-        if (more && has(1, j + 1)) issue_s(1, 2 * rj + 2);
-        if (more && one) tc_commit(&sh->empty[slot_of(2 * rj + 2)]);
+      if constexpr (kTwin) {
+        // Each entry feeds one product and is released right behind it.
+        const int n0 = je0 - js0, n1 = je1 - js1;
+        int e = 0;
+        auto release = [&]() {
+          if (one) tc_commit(&sh->empty[slot_of(e)]);
+          ++e;
+        };
+        if (ok) {
+          tc_fence_after();
+          issue_s(0, e);
+          release();
+          if (n1 > 0 && (ok = wait_full(e))) {
+            tc_fence_after();
+            issue_s(1, e);
+            release();
+          }
+        }
+        for (int st = 0; ok && st < n0; ++st) {
+          if (!(ok = wait_full(e) && issue_pv(0, e, st))) break;
+          release();
+          if (st + 1 < n0) {
+            if (!(ok = wait_full(e))) break;
+            tc_fence_after();
+            issue_s(0, e);  // behind PV0(st), which read the P that lies over S0
+            release();
+          }
+          if (st < n1) {
+            if (!(ok = wait_full(e) && issue_pv(1, e, st))) break;
+            release();
+          }
+          if (st + 1 < n1) {
+            if (!(ok = wait_full(e))) break;
+            tc_fence_after();
+            issue_s(1, e);
+            release();
+          }
+        }
+      } else {
+        // Tile j sits at ring index 2 * (j - jlo) (K) and one behind (V).
+        auto has = [&](int t, int j) {
+          return t == 0 ? (j >= js0 && j < je0) : (j >= js1 && j < je1);
+        };
+        if (ok) {
+          tc_fence_after();
+          if (has(0, jlo)) issue_s(0, 0);
+          if (has(1, jlo)) issue_s(1, 0);
+          if (one) tc_commit(&sh->empty[slot_of(0)]);
+        }
+        for (int rj = 0; ok && rj < jhi - jlo; ++rj) {
+          const int j = jlo + rj;
+          const bool more = j + 1 < jhi;
+          if (!(ok = wait_full(2 * rj + 1))) break;
+          if (more && !(ok = wait_full(2 * rj + 2))) break;
+          if (has(0, j) && !(ok = issue_pv(0, 2 * rj + 1, j - js0))) break;
+          // P_t(j) lies over S_t: the MMAs of one thread run in order, so S_t(j+1)
+          // is written only after P_t(j) has been read.
+          if (more && has(0, j + 1)) issue_s(0, 2 * rj + 2);
+          if (has(1, j) && !(ok = issue_pv(1, 2 * rj + 1, j - js1))) break;
+          if (one) tc_commit(&sh->empty[slot_of(2 * rj + 1)]);
+          if (more && has(1, j + 1)) issue_s(1, 2 * rj + 2);
+          if (more && one) tc_commit(&sh->empty[slot_of(2 * rj + 2)]);
+        }
       }
       // Every MMA issued above must finish before TMEM is released.
       if (one) tc_commit(&sh->mma_done);
       mbar_wait_drain(&sh->mma_done, 0, p.status);
     } else if (warp == 1) {
       // =============================================================== copies
-      // Lane u < 8 brings page u of a tile: its K, then its V slice, one untiled
-      // copy each, and its scales, which it reads a tile ahead.  Slots behind
-      // the keys keep what they held: their scores are masked, and the widening
-      // of such a tile lets no value that is no number pass.
+      // Lane 8e + u brings page u of every fourth entry e, one untiled copy, and
+      // its scale.  Page numbers are read two rounds of four entries ahead and
+      // scales one, so that neither's latency is waited for (read an entry ahead,
+      // they held the copies to 2.4 TB/s).  Slots behind the keys keep what they
+      // held: their scores are masked, and the widening of such a tile lets no
+      // value that is no number pass.
       const int *table = p.block_table + static_cast<size_t>(seq) * p.max_blocks;
-      const int u = lane & 7;
-      auto slice_of = [&](int j) {
-        const int pg = j * kPagesPerTile + u;
-        return j < jhi && pg * kPage < ck.n ? static_cast<long long>(table[pg]) * p.Hkv + hkv : -1LL;
-      };
+      const int u = lane & 7, e = lane >> 3;
       const float v_unit = __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23);
+      auto page_of = [&](int i) {  // of this lane's entry of the round from i on
+        bool v;
+        int j, slot;
+        if (i + e >= total) return -1;
+        entry<kTwin>(i + e, jlo, total, v, j, slot);
+        const int pg = j * kPagesPerTile + u;
+        return pg * kPage < ck.n ? table[pg] : -1;
+      };
+      auto scale_of = [&](int i, int pid) {
+        bool v;
+        int j, slot;
+        if (pid < 0) return 0.f;
+        entry<kTwin>(i + e, jlo, total, v, j, slot);
+        const size_t slice = static_cast<size_t>(pid) * p.Hkv + hkv;
+        return v ? p.v_scales[slice] * v_unit : p.k_scales[slice];
+      };
       int issued = 0;
-      long long slice = slice_of(jlo);
-      float ks = slice >= 0 ? p.k_scales[slice] : 0.f, vs = slice >= 0 ? p.v_scales[slice] : 0.f;
       bool go = true;
-      for (int j = jlo; go && j < jhi; ++j) {
-        const long long next = slice_of(j + 1);
-        const unsigned pages = __popc(__ballot_sync(0xffffffffu, slice >= 0) & 0xffu);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int i = 2 * (j - jlo) + kv, slot = i % C::NRAW;
+      int pid = page_of(0), pid1 = page_of(4);
+      float scale = scale_of(0, pid);
+      for (int i0 = 0; go && i0 < total; i0 += 4) {
+        const float scale1 = scale_of(i0 + 4, pid1);
+        const int pid2 = page_of(i0 + 8);
+        const unsigned live = __ballot_sync(0xffffffffu, pid >= 0);
+#pragma unroll 1
+        for (int k = 0; k < 4 && i0 + k < total; ++k) {
+          const int i = i0 + k, slot = i % C::NRAW;
           if (lane == 0 && i >= C::NRAW)
             go = mbar_wait(&sh->raw_empty[slot], (i / C::NRAW - 1) & 1, abort_flag, p.status);
           go = __shfl_sync(0xffffffffu, go, 0);
@@ -463,24 +643,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           if (i == EXATTN_TEST_WITHHOLD) go = false;
 #endif
           if (!go) break;
-          // (The softmax has read the K scales of eight tiles before: S of four
-          // tiles before this one was needed for its ring slot.)
-          if (lane < 8) {
-            if (kv == 0) sh->k_scale[(j - jlo) % kScaleRing][u] = ks;
-            else sh->v_scale[(j - jlo) % kScaleRing][u] = vs * v_unit;
-          }
+          bool v;
+          int j, scale_slot;
+          entry<kTwin>(i, jlo, total, v, j, scale_slot);
+          // (A scale slot comes round after eight tiles; the rings hold at most six
+          // between here and the softmax.)
+          if (e == k) (v ? sh->v_scale : sh->k_scale)[scale_slot][u] = scale;
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&sh->raw_full[slot], pages * (kPage * D));
+          if (lane == 0)
+            mbar_arrive_expect_tx(&sh->raw_full[slot], __popc((live >> (8 * k)) & 0xffu) * (kPage * D));
           __syncwarp();
-          if (lane < 8 && slice >= 0)
+          if (e == k && pid >= 0)
             bulk_load(smem + C::RAW_OFF + slot * C::RAW_BYTES + u * (kPage * D),
-                      (kv ? p.v_pages : p.k_pages) + static_cast<size_t>(slice) * (kPage * D), kPage * D,
-                      &sh->raw_full[slot]);
+                      (v ? p.v_pages : p.k_pages) + (static_cast<size_t>(pid) * p.Hkv + hkv) * (kPage * D),
+                      kPage * D, &sh->raw_full[slot]);
           issued = i + 1;
         }
-        slice = next;
-        ks = slice >= 0 ? p.k_scales[slice] : 0.f;
-        vs = slice >= 0 ? p.v_scales[slice] : 0.f;
+        pid = pid1;
+        scale = scale1;
+        pid1 = pid2;
       }
       // No copy may still be writing shared memory when the CTA exits.
       if (lane == 0)
@@ -519,78 +700,88 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       mbar_arrive(&sh->full[i % C::NST]);
       mbar_arrive(&sh->raw_empty[i % C::NRAW]);
     };
-    for (int rj = 0; rj < jhi - jlo; ++rj) {
-      const int j = jlo + rj;
-      {
-        const int i = 2 * rj;
-        if (!ready(i)) break;
-        const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
-        uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
+    auto widen_k = [&](int i) {
+      if (!ready(i)) return false;
+      const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
+      uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
 #pragma unroll
-        for (int u = 0; u < 2 * PASSES; ++u) {
-          const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
-          uint4 a, b;
-          widen4<FMT>(c.x, a.x, a.y);
-          widen4<FMT>(c.y, a.z, a.w);
-          widen4<FMT>(c.z, b.x, b.y);
-          widen4<FMT>(c.w, b.z, b.w);
-          put(dst, 2 * w * kPage + u * RPP + row, a, b);
-        }
-        done(i);
+      for (int u = 0; u < 2 * PASSES; ++u) {
+        const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
+        uint4 a, b;
+        widen4<FMT>(c.x, a.x, a.y);
+        widen4<FMT>(c.y, a.z, a.w);
+        widen4<FMT>(c.z, b.x, b.y);
+        widen4<FMT>(c.w, b.z, b.w);
+        put(dst, 2 * w * kPage + u * RPP + row, a, b);
       }
-      {
-        const int i = 2 * rj + 1;
-        if (!ready(i)) break;
-        const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
-        uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
-        const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[rj % kScaleRing][2 * w]);
-        // Tiles that some row sees only in part: their slot in v_bad, or -1.
-        const int edge = j >= edge_hi ? min(j - edge_hi, kEdge - 1)
-                                      : (p.window > 0 && j - edge_0 < kEdge ? kEdge + j - edge_0 : -1);
+      done(i);
+      return true;
+    };
+    auto widen_v = [&](int i, int j, int scale_slot) {
+      if (!ready(i)) return false;
+      const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
+      uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
+      const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[scale_slot][2 * w]);
+      // Tiles that some row sees only in part: their slot in v_bad, or -1.
+      const int edge = j >= edge_hi ? min(j - edge_hi, kEdge - 1)
+                                    : (p.window > 0 && j - edge_0 < kEdge ? kEdge + j - edge_0 : -1);
 #pragma unroll
-        for (int u = 0; u < 2 * PASSES; ++u) {
-          const float s = u < PASSES ? vs.x : vs.y;
-          const __half hi = __float2half_rn(s);
-          const __half lo = __float2half_rn(s - __half2float(hi));
-          const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
-          const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
-          uint32_t f[8];
-          widen4<FMT>(c.x, f[0], f[1]);
-          widen4<FMT>(c.y, f[2], f[3]);
-          widen4<FMT>(c.z, f[4], f[5]);
-          widen4<FMT>(c.w, f[6], f[7]);
+      for (int u = 0; u < 2 * PASSES; ++u) {
+        const float s = u < PASSES ? vs.x : vs.y;
+        const __half hi = __float2half_rn(s);
+        const __half lo = __float2half_rn(s - __half2float(hi));
+        const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+        const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
+        uint32_t f[8];
+        widen4<FMT>(c.x, f[0], f[1]);
+        widen4<FMT>(c.y, f[2], f[3]);
+        widen4<FMT>(c.z, f[4], f[5]);
+        widen4<FMT>(c.w, f[6], f[7]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __half2 x = as_h2(f[e]);
-            f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
-          }
-          put(dst, 2 * w * kPage + u * RPP + row, make_uint4(f[0], f[1], f[2], f[3]),
-              make_uint4(f[4], f[5], f[6], f[7]));
+        for (int e = 0; e < 8; ++e) {
+          const __half2 x = as_h2(f[e]);
+          f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
         }
-        if (edge >= 0) {
-          // What this lane stored, again: values that are no numbers leave.
+        put(dst, 2 * w * kPage + u * RPP + row, make_uint4(f[0], f[1], f[2], f[3]),
+            make_uint4(f[4], f[5], f[6], f[7]));
+      }
+      if (edge >= 0) {
+        // What this lane stored, again: values that are no numbers leave.
 #pragma unroll 1
-          for (int u = 0; u < 2 * PASSES; ++u) {
-            const int r = 2 * w * kPage + u * RPP + row;
+        for (int u = 0; u < 2 * PASSES; ++u) {
+          const int r = 2 * w * kPage + u * RPP + row;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              uint32_t *at = reinterpret_cast<uint32_t *>(dst + blk * CHUNK_BYTES + r * 128 + (((k0 + h) ^ (r & 7)) << 4));
-              bool bad = false;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t *at = reinterpret_cast<uint32_t *>(dst + blk * CHUNK_BYTES + r * 128 + (((k0 + h) ^ (r & 7)) << 4));
+            bool bad = false;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t f = at[e];
-                if ((f & 0x7c00u) == 0x7c00u) { f &= 0xffff0000u; bad = true; }
-                if ((f & 0x7c000000u) == 0x7c000000u) { f &= 0xffffu; bad = true; }
-                if (bad) at[e] = f;
-              }
-              if (bad) {
-                atomicOr(&sh->v_bad[edge][r >> 5], 1u << (r & 31));
-                sh->any_bad = 1;
-              }
+            for (int e = 0; e < 4; ++e) {
+              uint32_t f = at[e];
+              if ((f & 0x7c00u) == 0x7c00u) { f &= 0xffff0000u; bad = true; }
+              if ((f & 0x7c000000u) == 0x7c000000u) { f &= 0xffffu; bad = true; }
+              if (bad) at[e] = f;
+            }
+            if (bad) {
+              atomicOr(&sh->v_bad[edge][r >> 5], 1u << (r & 31));
+              sh->any_bad = 1;
             }
           }
         }
-        done(i);
+      }
+      done(i);
+      return true;
+    };
+    for (int i = 0; i < total; i += 2) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        bool v;
+        int j, scale_slot;
+        entry<kTwin>(i + k, jlo, total, v, j, scale_slot);
+        // (Without twins every other entry is a V, known when compiling.)
+        if (!((kTwin ? v : k == 1) ? widen_v(i + k, j, scale_slot) : widen_k(i + k))) {
+          i = total;
+          break;
+        }
       }
     }
   } else {
@@ -600,7 +791,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     const int quarter = warp & 3;    // TMEM lane quarter this warp may access
     const int r = quarter * 32 + lane;
     const int tl = r / p.heads;      // token of the tile; rows behind tokens * heads are idle
-    const int tok = tok0 + t * p.tokens + tl;
+    const int tok = tok0 + (kTwin ? 0 : t * p.tokens) + tl;
     const int hq = h0 + r - tl * p.heads;
     const bool valid = tl < p.tokens && tok < ck.nq;
     const int jst = t == 0 ? js0 : js1, jen = t == 0 ? je0 : je1;
@@ -665,7 +856,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       // The multipliers of each page's columns.
       float cp[kPagesPerTile];
       {
-        const float4 *ks = reinterpret_cast<const float4 *>(sh->k_scale[(j - jlo) % kScaleRing]);
+        const float4 *ks = reinterpret_cast<const float4 *>(sh->k_scale[(kTwin ? 2 * jj + t : j - jlo) % kScaleRing]);
         const float4 a = ks[0], b = ks[1];
         cp[0] = a.x * c_row; cp[1] = a.y * c_row; cp[2] = a.z * c_row; cp[3] = a.w * c_row;
         cp[4] = b.x * c_row; cp[5] = b.y * c_row; cp[6] = b.z * c_row; cp[7] = b.w * c_row;
@@ -780,39 +971,69 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       ok = mbar_wait(&sh->o_full[t], (nt - 1) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
     }
-    if (ok && (nt > 0 || p.nsplit > 1)) {
-      tc_fence_after();
-      // Weight zero for a row that saw no key here (a part of the keys only).
-      const bool seen = l != 0.f;
-      float a = seen ? scalbnf(1.0f / l, v_exp) : 0.f;
-      if (nt > 0 && *reinterpret_cast<volatile int *>(&sh->any_bad)) {
-        // A value that is no number was left out of the edge tiles: rows that
-        // see its key get NaN.
-        for (int e = 0; e < 2 * kEdge; ++e) {
-          const int j = e < kEdge ? edge_hi + e : edge_0 + e - kEdge;
-          if (j < jst || j >= jen || (e >= kEdge && j >= edge_hi)) continue;
-          const int hi = min(BN, ck.ctx + tok - j * BN + 1);
-          const int lo = p.window > 0 ? max(0, ck.ctx + tok - p.window + 1 - j * BN) : 0;
-          for (int i = lo; i < hi; ++i)
-            if (sh->v_bad[e][i >> 5] >> (i & 31) & 1u) a = NAN;
+    // A value that is no number was left out of the edge tiles: rows that see its
+    // key get NaN.
+    bool poison = false;
+    if (ok && nt > 0 && *reinterpret_cast<volatile int *>(&sh->any_bad)) {
+      for (int e = 0; e < 2 * kEdge; ++e) {
+        const int j = e < kEdge ? edge_hi + e : edge_0 + e - kEdge;
+        if (j < jst || j >= jen || (e >= kEdge && j >= edge_hi)) continue;
+        const int hi = min(BN, ck.ctx + tok - j * BN + 1);
+        const int lo = p.window > 0 ? max(0, ck.ctx + tok - p.window + 1 - j * BN) : 0;
+        for (int i = lo; i < hi; ++i) poison |= (sh->v_bad[e][i >> 5] >> (i & 31) & 1u) != 0;
+      }
+    }
+    // (l != 0 for a NaN too; 0 for a row that saw no key here: part of them only.)
+    float a0 = l != 0.f ? 1.f : 0.f, a1 = 0.f;  // weights of the O tiles
+    if constexpr (kTwin) {
+      // The tiles hold partial results of the same rows over disjoint keys: tile
+      // 0's threads join them, tile 1's publish m, l where their queries were.
+      float4 *xfer = reinterpret_cast<float4 *>(smem + C::TILE_BYTES);
+      if (t == 1) {
+        if (ok) {
+          xfer[r] = make_float4(m, l, poison ? 1.f : 0.f, 0.f);
+          tc_fence_before();
+          mbar_arrive(&sh->mrg_full);
+        }
+        ok = false;  // nothing more for this warpgroup
+      } else if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sh->mrg_full, 0, abort_flag, p.status));
+        if (ok) {
+          tc_fence_after();
+          const float4 x = xfer[r];
+          const float mm = fmaxf(m, x.x);
+          a0 = l != 0.f ? ex2(m - mm) : 0.f;
+          a1 = x.y != 0.f ? ex2(x.x - mm) : 0.f;
+          l = (l != 0.f ? a0 * l : 0.f) + (x.y != 0.f ? a1 * x.y : 0.f);
+          m = mm;
+          poison |= x.z != 0.f;
         }
       }
+    }
+    if (ok && (nt > 0 || p.split)) {
+      tc_fence_after();
+      const bool seen = l != 0.f;
+      const float inv = poison ? NAN : (seen ? scalbnf(1.0f / l, v_exp) : 0.f);
       const float l2 = seen ? m + log2f(l) : -INFINITY;
-      const size_t prow = out_row * p.nsplit + part;
+      const bool use0 = nt > 0 && a0 != 0.f, use1 = kTwin && a1 != 0.f;
+      a0 *= inv;
+      a1 *= inv;
+      const size_t prow = static_cast<size_t>(lin) * p.rows_cap + (kTwin ? 0 : t * p.tokens * p.heads) + r;
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t ov[32];
-        if (nt > 0) {  // (the same for the whole warp)
-          tmem_ld32(o_addr + cc * 32, ov);
-          tmem_ld_wait(ov);
+        uint32_t ov[32], ov1[kTwin ? 32 : 1];
+        tmem_ld32(o_addr + cc * 32, ov);
+        if constexpr (kTwin) tmem_ld32(o_addr + 128 + cc * 32, ov1);
+        tmem_ld_wait(ov);
+        if constexpr (kTwin) tmem_ld_wait(ov1);
+        // (A tile that has seen nothing may hold anything.)
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            ov[i] = seen ? __float_as_uint(__uint_as_float(ov[i]) * a) : 0u;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = 0u;
+        for (int i = 0; i < 32; ++i) {
+          float x = use0 ? __uint_as_float(ov[i]) * a0 : 0.f;
+          if constexpr (kTwin) x += use1 ? __uint_as_float(ov1[i]) * a1 : 0.f;
+          ov[i] = __float_as_uint(x);
         }
-        if (valid && p.nsplit == 1) {
+        if (valid && !p.split) {
           uint4 *dst = reinterpret_cast<uint4 *>(p.o + out_row * D + cc * 32);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -829,7 +1050,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         }
       }
       if (valid) {
-        if (p.nsplit == 1) p.lse[out_row] = l2 * 0.6931471805599453f;
+        if (!p.split) p.lse[out_row] = l2 * 0.6931471805599453f;
         else p.l2_part[prow] = l2;
       }
     }
@@ -855,20 +1076,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_q8_join_kernel(const 
   Chunk ck;
   if (h >= p.Hq || !chunk_of(p, s, ck) || tok >= ck.nq) return;
   const size_t row = static_cast<size_t>(ck.q0 + tok) * p.Hq + h;
-  const float *l2 = p.l2_part + row * p.nsplit;
+  // The CTAs that hold this row, and its place among theirs.
+  const int pair = tok / p.span, group = h / p.heads;
+  const int parts = p.plan[p.S + s];
+  const int cta = p.plan[s] + (pair * (p.Hq / p.heads) + group) * parts;
+  const int at = (tok - pair * p.span) * p.heads + h - group * p.heads;
+  const size_t slot = static_cast<size_t>(cta) * p.rows_cap + at;
   float top = -INFINITY;
-  for (int i = lane; i < p.nsplit; i += 32) top = fmaxf(top, l2[i]);
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.l2_part[slot + static_cast<size_t>(i) * p.rows_cap]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   constexpr int E = D / 32;  // consecutive elements of this lane
   float acc[E], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int i = 0; i < p.nsplit; ++i) {
-    const float w = ex2(l2[i] - top);  // NaN where a part failed
-    if (w == 0.f) continue;
+  for (int i = 0; i < parts; ++i) {
+    const size_t from = slot + static_cast<size_t>(i) * p.rows_cap;
+    const float w = ex2(p.l2_part[from] - top);  // NaN where a part failed
     sum += w;
-    const float *o = p.o_part + (row * p.nsplit + i) * D + lane * E;
+    const float *o = p.o_part + from * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const float2 v = *reinterpret_cast<const float2 *>(o + e);
@@ -883,9 +1109,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_q8_join_kernel(const 
   if (lane == 0) p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// How a call is cut: query heads per CTA, tokens per tile, pairs, parts.
+// How a call is cut: query heads per CTA, tokens per tile and CTA, CTAs.
 struct Cut {
-  int heads, tokens, pairs, nsplit;
+  int heads, tokens, span, pairs, rows_cap;
+  bool twin, split;
   long long ctas;
 };
 Cut cut(int S, int Hq, int Hkv, int max_q, int max_blocks) {
@@ -895,18 +1122,23 @@ Cut cut(int S, int Hq, int Hkv, int max_q, int max_blocks) {
   while (G % n) ++n;
   c.heads = G / n;
   c.tokens = BM / c.heads;
-  c.pairs = (max_q + 2 * c.tokens - 1) / (2 * c.tokens);
-  const long long base = static_cast<long long>(S) * Hkv * n * c.pairs;
-  // Parts of the keys: as many as fill the SMs, each of two key tiles at least.
-  const int tiles = (max_blocks + kPagesPerTile - 1) / kPagesPerTile;
-  long long ns = base < kSMs ? kSMs / base : 1;
-  if (ns > (tiles + 1) / 2) ns = (tiles + 1) / 2;
-  c.nsplit = ns < 1 ? 1 : static_cast<int>(ns);
-  c.ctas = base * c.nsplit;
+  const bool many = max_blocks > kPagesPerTile;  // more than one key tile
+  // Chunks that fit one row tile: both tiles take the same rows and half the
+  // keys each, which overlaps what one tile alone does in turn (20 rows over
+  // 8 K to 32 K keys, 4 sequences: see the table of operators).
+  c.twin = many && max_q <= c.tokens;
+  c.span = c.twin ? c.tokens : 2 * c.tokens;
+  c.pairs = (max_q + c.span - 1) / c.span;
+  c.rows_cap = (max_q < c.span ? max_q : c.span) * c.heads;
+  c.ctas = static_cast<long long>(S) * Hkv * n * c.pairs;
+  // Fewer work items than SMs: their keys are split over as many CTAs.
+  c.split = many && c.ctas < kSMs;
+  if (c.split) c.ctas = kSMs;
   return c;
 }
+size_t plan_bytes(int S) { return (2 * S * sizeof(int) + 255) / 256 * 256; }
 
-template <int D, int FMT, bool kAlibi>
+template <int D, int FMT, bool kAlibi, bool kTwin>
 attn_status_t launch(const Params &p, long long ctas, cudaStream_t stream) {
   using C = Cfg<D>;
   // The attribute belongs to the kernel on one device: set once on each.
@@ -918,15 +1150,15 @@ attn_status_t launch(const Params &p, long long ctas, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lock(mutex);
     if (!set[dev]) {
-      if (cudaFuncSetAttribute(prefill_q8_kernel<D, FMT, kAlibi>,
+      if (cudaFuncSetAttribute(prefill_q8_kernel<D, FMT, kAlibi, kTwin>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
         return ATTN_ERR_CUDA;
       set[dev] = true;
     }
   }
-  prefill_q8_kernel<D, FMT, kAlibi><<<static_cast<unsigned>(ctas), NUM_THREADS, C::SMEM_BYTES, stream>>>(p);
+  prefill_q8_kernel<D, FMT, kAlibi, kTwin><<<static_cast<unsigned>(ctas), NUM_THREADS, C::SMEM_BYTES, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  if (p.nsplit == 1) return ATTN_OK;
+  if (!p.split) return ATTN_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.S) * p.max_q, (p.Hq + kJoinWarps - 1) / kJoinWarps);
   cfg.blockDim = dim3(kJoinWarps * 32);
@@ -940,12 +1172,19 @@ attn_status_t launch(const Params &p, long long ctas, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+template <int D, int FMT>
+attn_status_t launch_variant(const Params &p, const Cut &c, cudaStream_t stream) {
+  if (p.slopes)
+    return c.twin ? launch<D, FMT, true, true>(p, c.ctas, stream) : launch<D, FMT, true, false>(p, c.ctas, stream);
+  return c.twin ? launch<D, FMT, false, true>(p, c.ctas, stream) : launch<D, FMT, false, false>(p, c.ctas, stream);
+}
+
 }  // namespace
 
 size_t prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q, int d, int max_blocks) {
   const Cut c = cut(S, Hq, Hkv, max_q, max_blocks);
-  if (c.nsplit == 1) return 0;
-  return static_cast<size_t>(T) * Hq * c.nsplit * (d + 1) * sizeof(float);
+  if (!c.split || T == 0) return 0;
+  return plan_bytes(S) + static_cast<size_t>(kSMs) * c.rows_cap * (d + 1) * sizeof(float);
 }
 
 attn_status_t launch_prefill_paged_q8(const void *q, const void *k_pages, const void *v_pages,
@@ -957,8 +1196,8 @@ attn_status_t launch_prefill_paged_q8(const void *q, const void *k_pages, const 
                                       unsigned *status) {
   const Cut c = cut(S, Hq, Hkv, max_q, max_blocks);
   if (c.ctas > 0x7fffffffLL || (Hq + kJoinWarps - 1) / kJoinWarps > 65535 ||
-      static_cast<long long>(c.pairs) * (Hq / c.heads) * c.nsplit > 0x7fffffffLL ||
-      (c.nsplit > 1 && static_cast<long long>(S) * max_q > 0x7fffffffLL))
+      static_cast<long long>(c.pairs) * (Hq / c.heads) > 0x7fffffffLL ||
+      (c.split && static_cast<long long>(S) * max_q > 0x7fffffffLL))
     return ATTN_ERR_INVALID_ARG;
   Params p{};
   p.q = static_cast<const __nv_bfloat16 *>(q);
@@ -971,9 +1210,10 @@ attn_status_t launch_prefill_paged_q8(const void *q, const void *k_pages, const 
   p.cu_q = cu_q;
   p.o = static_cast<__nv_bfloat16 *>(o);
   p.lse = lse;
-  if (c.nsplit > 1) {
-    p.o_part = static_cast<float *>(workspace);
-    p.l2_part = p.o_part + static_cast<size_t>(T) * Hq * c.nsplit * d;
+  if (c.split) {
+    p.plan = static_cast<int *>(workspace);
+    p.o_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan_bytes(S));
+    p.l2_part = p.o_part + static_cast<size_t>(kSMs) * c.rows_cap * d;
   }
   p.slopes = slopes;
   p.status = status;
@@ -986,21 +1226,16 @@ attn_status_t launch_prefill_paged_q8(const void *q, const void *k_pages, const 
   p.num_pages = num_pages;
   p.heads = c.heads;
   p.tokens = c.tokens;
+  p.span = c.span;
   p.pairs = c.pairs;
-  p.nsplit = c.nsplit;
+  p.split = c.split;
+  p.rows_cap = c.rows_cap;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = window;
   const bool e4m3 = kv_format == ATTN_KV_E4M3;
-  if (d == 128) {
-    if (slopes) return e4m3 ? launch<128, ATTN_KV_E4M3, true>(p, c.ctas, stream)
-                            : launch<128, ATTN_KV_INT8, true>(p, c.ctas, stream);
-    return e4m3 ? launch<128, ATTN_KV_E4M3, false>(p, c.ctas, stream)
-                : launch<128, ATTN_KV_INT8, false>(p, c.ctas, stream);
-  }
-  if (slopes) return e4m3 ? launch<64, ATTN_KV_E4M3, true>(p, c.ctas, stream)
-                          : launch<64, ATTN_KV_INT8, true>(p, c.ctas, stream);
-  return e4m3 ? launch<64, ATTN_KV_E4M3, false>(p, c.ctas, stream)
-              : launch<64, ATTN_KV_INT8, false>(p, c.ctas, stream);
+  if (d == 128)
+    return e4m3 ? launch_variant<128, ATTN_KV_E4M3>(p, c, stream) : launch_variant<128, ATTN_KV_INT8>(p, c, stream);
+  return e4m3 ? launch_variant<64, ATTN_KV_E4M3>(p, c, stream) : launch_variant<64, ATTN_KV_INT8>(p, c, stream);
 }
 
 }  // namespace exattn
