@@ -29,11 +29,12 @@
 //  * Exactness.  Codes are exact in f16.  Queries are scaled by a power of two
 //    per row before rounding to f16, exact for elements within 2^28 of the
 //    row's largest.  The K scale multiplies the f32 scores, per page.  The V
-//    scale multiplies the code on its way to f16, rounded once: v = fma(code,
-//    hi, code * lo) with hi + lo the scale to 22 bits, relative to a power of
-//    two just above the largest V scale of the CTA's pages.  (A page whose V
-//    scale is under 2^-19 of that largest one loses bits of its own values.)
-//    P is rounded to f16 (2^-11 of each, against bf16's 2^-8 of the output).
+//    scale, relative to a power of two just above the largest V scale of the
+//    CTA's pages, multiplies the code on its way to f16, rounded once: v =
+//    fma(code, hi, code * lo) with hi + lo the scale to 22 bits; or (twin tiles)
+//    P before it is rounded to f16.  (A page whose V scale is under 2^-19 of that
+//    largest one loses bits of its own values.)  P is rounded to f16 (2^-11 of
+//    each, against bf16's 2^-8 of the output).
 //  * Few rows and long keys: when the row tiles alone leave SMs idle, each
 //    tile's keys are split over several CTAs, which write normalised partials
 //    and their log2-sum-exps to the workspace; a second kernel, scheduled
@@ -176,9 +177,11 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &a, uint32_t &b) {
 }
 
 // Half a score row (64 columns, four pages) -> 32 f16 pairs of P = 2^(s*c - m), c
-// the multiplier of the columns' page; returns the part of the row sum.
-__device__ __forceinline__ float exp_half(const uint32_t (&sv)[64], const float *c, float m,
-                                          uint32_t (&pk)[32]) {
+// the multiplier of the columns' page, and (kScaled) times their pages' V scale v;
+// returns the part of the row sum, which has no V scale.
+template <bool kScaled>
+__device__ __forceinline__ float exp_half(const uint32_t (&sv)[64], const float *c, const float *v,
+                                          float m, uint32_t (&pk)[32]) {
   const float2 nm2 = make_float2(-m, -m);
   float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
 #pragma unroll
@@ -186,10 +189,15 @@ __device__ __forceinline__ float exp_half(const uint32_t (&sv)[64], const float 
     const float2 c2 = make_float2(c[i / kPage], c[i / kPage]);
     const float2 x0 = fma2(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), c2, nm2);
     const float2 x1 = fma2(make_float2(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), c2, nm2);
-    const float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
-    const float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
+    float2 p0 = make_float2(ex2(x0.x), ex2(x0.y));
+    float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
     sum_a = add2(sum_a, p0);
     sum_b = add2(sum_b, p1);
+    if constexpr (kScaled) {
+      const float2 v2 = make_float2(v[i / kPage], v[i / kPage]), z2 = make_float2(0.f, 0.f);
+      p0 = fma2(p0, v2, z2);
+      p1 = fma2(p1, v2, z2);
+    }
     pk[i >> 1] = pack_f16x2(p0.x, p0.y);
     pk[(i >> 1) + 1] = pack_f16x2(p1.x, p1.y);
   }
@@ -615,20 +623,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         const int pg = j * kPagesPerTile + u;
         return pg * kPage < ck.n ? table[pg] : -1;
       };
+      // The scale of its tensor; twin tiles take both with K, since the softmax
+      // applies V's.
       auto scale_of = [&](int i, int pid) {
         bool v;
         int j, slot;
-        if (pid < 0) return 0.f;
+        float2 x = make_float2(0.f, 0.f);
+        if (pid < 0) return x;
         entry<kTwin>(i + e, jlo, total, v, j, slot);
         const size_t slice = static_cast<size_t>(pid) * p.Hkv + hkv;
-        return v ? p.v_scales[slice] * v_unit : p.k_scales[slice];
+        if (!v) x.x = p.k_scales[slice];
+        if (kTwin ? !v : v) x.y = p.v_scales[slice] * v_unit;
+        return x;
       };
       int issued = 0;
       bool go = true;
       int pid = page_of(0), pid1 = page_of(4);
-      float scale = scale_of(0, pid);
+      float2 scale = scale_of(0, pid);
       for (int i0 = 0; go && i0 < total; i0 += 4) {
-        const float scale1 = scale_of(i0 + 4, pid1);
+        const float2 scale1 = scale_of(i0 + 4, pid1);
         const int pid2 = page_of(i0 + 8);
         const unsigned live = __ballot_sync(0xffffffffu, pid >= 0);
 #pragma unroll 1
@@ -648,7 +661,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           entry<kTwin>(i, jlo, total, v, j, scale_slot);
           // (A scale slot comes round after eight tiles; the rings hold at most six
           // between here and the softmax.)
-          if (e == k) (v ? sh->v_scale : sh->k_scale)[scale_slot][u] = scale;
+          if (e == k) {
+            if (!v) sh->k_scale[scale_slot][u] = scale.x;
+            if (kTwin ? !v : v) sh->v_scale[scale_slot][u] = scale.y;
+          }
           __syncwarp();
           if (lane == 0)
             mbar_arrive_expect_tx(&sh->raw_full[slot], __popc((live >> (8 * k)) & 0xffu) * (kPage * D));
@@ -690,6 +706,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       *reinterpret_cast<uint4 *>(line + ((k0 ^ x) << 4)) = a;
       *reinterpret_cast<uint4 *>(line + (((k0 + 1) ^ x) << 4)) = b;
     };
+    // A lane's share of a raw tile, unscaled.  The compiler keeps loads and stores
+    // of shared memory in order, so that one load at a time waits for the store
+    // before it (900 cycles a tile); twin tiles, where this is what bounds the
+    // kernel, load all of it first (700; beside two busy softmaxes that gains
+    // nothing: 560 us against 549 for 16 chunks of 512).
+    auto widen_plain = [&](const uint8_t *src, uint8_t *dst) {
+      constexpr int A = kTwin ? 2 * PASSES : 1;
+#pragma unroll
+      for (int u0 = 0; u0 < 2 * PASSES; u0 += A) {
+        uint4 c[A];
+#pragma unroll
+        for (int u = 0; u < A; ++u) c[u] = *reinterpret_cast<const uint4 *>(src + (u0 + u) * 512);
+#pragma unroll
+        for (int u = 0; u < A; ++u) {
+          uint4 a, b;
+          widen4<FMT>(c[u].x, a.x, a.y);
+          widen4<FMT>(c[u].y, a.z, a.w);
+          widen4<FMT>(c[u].z, b.x, b.y);
+          widen4<FMT>(c[u].w, b.z, b.w);
+          put(dst, 2 * w * kPage + (u0 + u) * RPP + row, a, b);
+        }
+      }
+    };
     // Raw entry i is in its slot, and the ring's slot for it is free.
     auto ready = [&](int i) {
       if (!mbar_wait(&sh->raw_full[i % C::NRAW], (i / C::NRAW) & 1, abort_flag, p.status)) return false;
@@ -704,16 +743,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       if (!ready(i)) return false;
       const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
       uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
-#pragma unroll
-      for (int u = 0; u < 2 * PASSES; ++u) {
-        const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
-        uint4 a, b;
-        widen4<FMT>(c.x, a.x, a.y);
-        widen4<FMT>(c.y, a.z, a.w);
-        widen4<FMT>(c.z, b.x, b.y);
-        widen4<FMT>(c.w, b.z, b.w);
-        put(dst, 2 * w * kPage + u * RPP + row, a, b);
-      }
+      widen_plain(src, dst);
       done(i);
       return true;
     };
@@ -721,29 +751,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       if (!ready(i)) return false;
       const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
       uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
-      const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[scale_slot][2 * w]);
       // Tiles that some row sees only in part: their slot in v_bad, or -1.
       const int edge = j >= edge_hi ? min(j - edge_hi, kEdge - 1)
                                     : (p.window > 0 && j - edge_0 < kEdge ? kEdge + j - edge_0 : -1);
+      if constexpr (kTwin) {
+        widen_plain(src, dst);
+      } else {
+        const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[scale_slot][2 * w]);
 #pragma unroll
-      for (int u = 0; u < 2 * PASSES; ++u) {
-        const float s = u < PASSES ? vs.x : vs.y;
-        const __half hi = __float2half_rn(s);
-        const __half lo = __float2half_rn(s - __half2float(hi));
-        const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
-        const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
-        uint32_t f[8];
-        widen4<FMT>(c.x, f[0], f[1]);
-        widen4<FMT>(c.y, f[2], f[3]);
-        widen4<FMT>(c.z, f[4], f[5]);
-        widen4<FMT>(c.w, f[6], f[7]);
+        for (int u = 0; u < 2 * PASSES; ++u) {
+          const float s = u < PASSES ? vs.x : vs.y;
+          const __half hi = __float2half_rn(s);
+          const __half lo = __float2half_rn(s - __half2float(hi));
+          const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
+          const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
+          uint32_t f[8];
+          widen4<FMT>(c.x, f[0], f[1]);
+          widen4<FMT>(c.y, f[2], f[3]);
+          widen4<FMT>(c.z, f[4], f[5]);
+          widen4<FMT>(c.w, f[6], f[7]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const __half2 x = as_h2(f[e]);
-          f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
+          for (int e = 0; e < 8; ++e) {
+            const __half2 x = as_h2(f[e]);
+            f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
+          }
+          put(dst, 2 * w * kPage + u * RPP + row, make_uint4(f[0], f[1], f[2], f[3]),
+              make_uint4(f[4], f[5], f[6], f[7]));
         }
-        put(dst, 2 * w * kPage + u * RPP + row, make_uint4(f[0], f[1], f[2], f[3]),
-            make_uint4(f[4], f[5], f[6], f[7]));
       }
       if (edge >= 0) {
         // What this lane stored, again: values that are no numbers leave.
@@ -835,6 +869,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     const bool idle = !__any_sync(0xffffffffu, valid);
     float m = -INFINITY;  // reference max, in log2 units of scaled scores
     float l = 0.f;
+    bool poison = false;  // the row sees a value that is no number and was left out
     bool ok = true;
     for (int jj = 0; jj < nt; ++jj) {
       const int j = jst + jj;
@@ -861,6 +896,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         cp[0] = a.x * c_row; cp[1] = a.y * c_row; cp[2] = a.z * c_row; cp[3] = a.w * c_row;
         cp[4] = b.x * c_row; cp[5] = b.y * c_row; cp[6] = b.z * c_row; cp[7] = b.w * c_row;
       }
+      // Twin tiles: the V scales, which P takes here.
+      float vp[kTwin ? kPagesPerTile : 1];
+      if constexpr (kTwin) {
+        const float4 *vs = reinterpret_cast<const float4 *>(sh->v_scale[(2 * jj + t) % kScaleRing]);
+        const float4 a = vs[0], b = vs[1];
+        vp[0] = a.x; vp[1] = a.y; vp[2] = a.z; vp[3] = a.w;
+        vp[4] = b.x; vp[5] = b.y; vp[6] = b.z; vp[7] = b.w;
+        const float any = (vp[0] + vp[1] + vp[2] + vp[3]) + (vp[4] + vp[5] + vp[6] + vp[7]);
+        if (!(fabsf(any) <= 3.4028235e38f)) {
+          // A scale that is no number: rows that see its page get NaN, and no
+          // zero P is multiplied by it.
+#pragma unroll
+          for (int g = 0; g < kPagesPerTile; ++g)
+            if (!(fabsf(vp[g]) <= 3.4028235e38f)) {
+              poison |= lo < kPage * (g + 1) && hi > kPage * g;
+              vp[g] = 0.f;
+            }
+        }
+      }
       // The row goes in halves of 64 columns, and the first half's P is handed
       // on while the second is worked on.  P of columns 0-63 lies over S columns
       // 0-31, that of 64-127 over 32-63.
@@ -873,7 +927,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         // max-first step below would have kept the reference too.
         tmem_ld64(s_addr, sv);
         tmem_ld_wait64(sv);
-        const float l0 = exp_half(sv, cp, m, pk);
+        const float l0 = exp_half<kTwin>(sv, cp, vp, m, pk);
         if (__all_sync(0xffffffffu, l0 <= 255.0f)) {
           first_done = true;
           tmem_ld64(s_addr + 64, sv);
@@ -883,7 +937,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           mbar_arrive(&sh->p_half[t]);
           l += l0;
           tmem_ld_wait64(sv);
-          const float l1 = exp_half(sv, cp + 4, m, pk);
+          const float l1 = exp_half<kTwin>(sv, cp + 4, vp + (kTwin ? 4 : 0), m, pk);
           if (__all_sync(0xffffffffu, l1 <= 255.0f)) {
             l += l1;
             store_half(s_addr + 32, pk);
@@ -960,7 +1014,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
 #pragma unroll 1
       for (int h = first_done; h < 2; ++h) {
         scaled_half(h);
-        l += exp_half(sv, ones, m_use, pk);
+        float vh[4];
+        if constexpr (kTwin) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vh[i] = h ? vp[4 + i] : vp[i];
+        }
+        l += exp_half<kTwin>(sv, ones, vh, m_use, pk);
         store_half(s_addr + 32 * h, pk);
         tmem_st_wait();
         tc_fence_before();
@@ -971,9 +1030,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       ok = mbar_wait(&sh->o_full[t], (nt - 1) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
     }
-    // A value that is no number was left out of the edge tiles: rows that see its
-    // key get NaN.
-    bool poison = false;
+    // Codes that are no numbers were left out of the edge tiles: rows that see
+    // their keys get NaN.
     if (ok && nt > 0 && *reinterpret_cast<volatile int *>(&sh->any_bad)) {
       for (int e = 0; e < 2 * kEdge; ++e) {
         const int j = e < kEdge ? edge_hi + e : edge_0 + e - kEdge;
