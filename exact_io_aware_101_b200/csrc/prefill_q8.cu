@@ -70,20 +70,23 @@ constexpr int kSMs = 148;
 constexpr int kScaleRing = 8;  // tiles whose page scales are kept in shared memory
 constexpr int kEdge = 4;       // tiles that a row may see in part, at either end of the walk
 
-template <int D>
+template <int D, bool kTwin>
 struct Cfg {
   static constexpr int TILE_BYTES = BM * D * 2;  // a Q, K or V tile in f16
-  static constexpr int NST = (D == 64) ? 6 : 3;  // ring slots
+  static constexpr int NQ = kTwin ? 1 : 2;       // Q tiles (twin tiles have one)
+  static constexpr int NST = (D == 64 ? 8 : 5) - NQ;  // ring slots: what is left
   static constexpr int RAW_BYTES = BN * D;       // a K or V tile in codes
   static constexpr int NRAW = 4;                 // raw slots
-  static constexpr int RING_OFF = 2 * TILE_BYTES;
+  static constexpr int RING_OFF = NQ * TILE_BYTES;
   static constexpr int RAW_OFF = RING_OFF + NST * TILE_BYTES;
-  static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW_BYTES;
+  static constexpr int XFER_OFF = RAW_OFF + NRAW * RAW_BYTES;  // twin: m and l of tile 1's rows
+  static constexpr int BAR_OFF = XFER_OFF + (kTwin ? 1024 : 0);
   static constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;  // + 1 KB align slack
   static constexpr uint32_t IDESC_QK =  // as idesc_bf16_f32, with both operand formats 0 (f16)
       idesc_bf16_f32(BM, BN, false, false) & ~((7u << 7) | (7u << 10));
   static constexpr uint32_t IDESC_PV =
       idesc_bf16_f32(BM, D, false, true) & ~((7u << 7) | (7u << 10));
+  static_assert(SMEM_BYTES <= 232448 && NST >= 3 && NST <= 8, "fits an SM");
 };
 
 struct Shared {
@@ -104,6 +107,7 @@ struct Shared {
   unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with a NaN or infinite value
   unsigned v_top;                      // largest finite |V scale| of the CTA's pages, as bits
   int any_bad;
+  unsigned poison1[BM / 32];  // twin: rows of tile 1 that see a value left out
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -322,7 +326,7 @@ __device__ __forceinline__ void entry(int i, int jlo, int total, bool &v, int &j
 
 template <int D, int FMT, bool kAlibi, bool kTwin>
 __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params p) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kTwin>;
   grid_dependents_launch();  // the joining kernel may be scheduled behind this grid
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       const uint64_t kdesc0 = sdesc_sw128(ring_base, 16, 1024);
       const uint64_t vdesc0 = sdesc_sw128(ring_base, CHUNK_BYTES, 1024);
       auto issue_s = [&](int t, int kidx) {  // S_t = Q_t K^T
-        const uint64_t qd = qdesc0 + ((t * C::TILE_BYTES) >> 4);
+        const uint64_t qd = qdesc0 + (((kTwin ? 0 : t) * C::TILE_BYTES) >> 4);
         const uint64_t kd = kdesc0 + ((slot_of(kidx) * C::TILE_BYTES) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -536,7 +540,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       };
       bool ok = wait_full(0);
       if (ok && js0 < je0) ok = mbar_wait(&sh->q_full[0], 0, abort_flag, p.status);
-      if (ok && js1 < je1) ok = mbar_wait(&sh->q_full[1], 0, abort_flag, p.status);
+      if (!kTwin && ok && js1 < je1) ok = mbar_wait(&sh->q_full[1], 0, abort_flag, p.status);
       if constexpr (kTwin) {
         // Each entry feeds one product and is released right behind it.
         const int n0 = je0 - js0, n1 = je1 - js1;
@@ -836,7 +840,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     const size_t out_row = static_cast<size_t>(ck.q0 + (valid ? tok : 0)) * p.Hq + hq;
     float c_row = p.scale_log2;  // from a raw score to log2 units, but for the page's K scale
     if (nt > 0) {
-      // This row of Q to f16, its largest element in [2^14, 2^15).
+      // This row of Q to f16, its largest element in [2^14, 2^15).  (Twin tiles
+      // have one Q tile, which tile 0's threads fill.)
       uint4 u[D / 8];
       uint32_t top = 0;
 #pragma unroll
@@ -851,18 +856,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
       c_row *= __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
       uint8_t *line = smem + t * C::TILE_BYTES + r * 128;
+      if (!kTwin || t == 0) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t in[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        uint32_t f[4];
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t in[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          uint32_t f[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          f[e] = pack_f16x2(__uint_as_float(in[e] << 16) * up, __uint_as_float(in[e] & 0xffff0000u) * up);
-        *reinterpret_cast<uint4 *>(line + (i >> 3) * CHUNK_BYTES + (((i & 7) ^ (r & 7)) << 4)) =
-            make_uint4(f[0], f[1], f[2], f[3]);
+          for (int e = 0; e < 4; ++e)
+            f[e] = pack_f16x2(__uint_as_float(in[e] << 16) * up, __uint_as_float(in[e] & 0xffff0000u) * up);
+          *reinterpret_cast<uint4 *>(line + (i >> 3) * CHUNK_BYTES + (((i & 7) ^ (r & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        fence_async_shared();
+        mbar_arrive(&sh->q_full[t]);
       }
-      fence_async_shared();
-      mbar_arrive(&sh->q_full[t]);
     }
     const float slope2 = kAlibi && valid ? p.slopes[hq] * 1.4426950408889634f : 0.f;
     // A warp without a row of its own (a chunk of a few tokens) only hands on.
@@ -1045,12 +1052,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     float a0 = l != 0.f ? 1.f : 0.f, a1 = 0.f;  // weights of the O tiles
     if constexpr (kTwin) {
       // The tiles hold partial results of the same rows over disjoint keys: tile
-      // 0's threads join them, tile 1's publish m, l where their queries were.
-      float4 *xfer = reinterpret_cast<float4 *>(smem + C::TILE_BYTES);
+      // 1's threads publish their m and l, and tile 0's join them.
+      float2 *xfer = reinterpret_cast<float2 *>(smem + C::XFER_OFF);
       if (t == 1) {
         if (ok) {
-          xfer[r] = make_float4(m, l, poison ? 1.f : 0.f, 0.f);
+          xfer[r] = make_float2(m, l);
+          const unsigned rows = __ballot_sync(0xffffffffu, poison);
+          if (lane == 0) sh->poison1[quarter] = rows;
           tc_fence_before();
+          __syncwarp();
           mbar_arrive(&sh->mrg_full);
         }
         ok = false;  // nothing more for this warpgroup
@@ -1058,13 +1068,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         ok = __all_sync(0xffffffffu, mbar_wait(&sh->mrg_full, 0, abort_flag, p.status));
         if (ok) {
           tc_fence_after();
-          const float4 x = xfer[r];
+          const float2 x = xfer[r];
           const float mm = fmaxf(m, x.x);
           a0 = l != 0.f ? ex2(m - mm) : 0.f;
           a1 = x.y != 0.f ? ex2(x.x - mm) : 0.f;
           l = (l != 0.f ? a0 * l : 0.f) + (x.y != 0.f ? a1 * x.y : 0.f);
           m = mm;
-          poison |= x.z != 0.f;
+          poison |= (sh->poison1[quarter] >> lane & 1u) != 0;
         }
       }
     }
@@ -1198,7 +1208,7 @@ size_t plan_bytes(int S) { return (2 * S * sizeof(int) + 255) / 256 * 256; }
 
 template <int D, int FMT, bool kAlibi, bool kTwin>
 attn_status_t launch(const Params &p, long long ctas, cudaStream_t stream) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kTwin>;
   // The attribute belongs to the kernel on one device: set once on each.
   constexpr int kMaxDevices = 64;
   static std::mutex mutex;
