@@ -30,6 +30,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -206,20 +207,24 @@ def _is(t, dtype, ndim: int, index: int) -> bool:
     return (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.get_device() == index)
 
 
-class _OnDevice:
-    """The current CUDA device for one call, switched only where it is another."""
+class _Call:
+    """One entry point of the library, called with the tensors' device current (switched only
+    where another is) and its error raised."""
 
-    def __init__(self, index: int):
-        self.index = index
+    def __init__(self, name: str):
+        self.name, self.fn = name, None
 
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *_):
-        if self.back != self.index:
-            torch.cuda.set_device(self.back)
+    def __call__(self, index: int, *args):
+        if self.fn is None:
+            self.fn = getattr(library(), self.name)
+        back = torch._C._cuda_getDevice()
+        if back == index:
+            rc = self.fn(*args)
+        else:
+            with torch.cuda.device(index):
+                rc = self.fn(*args)
+        if rc != 0:
+            raise AttnError(rc, self.name)
 
 
 def _raise(rc: int, what: str):
@@ -590,42 +595,59 @@ def _q8_cache(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
     that they are reported the same way on any device."""
     if kv_format not in KV_FORMATS:
         raise ValueError("kv_format must be one of %s" % sorted(KV_FORMATS))
-    for name, t, nd in (("k_pages", k_pages, 4), ("v_pages", v_pages, 4),
-                        ("k_scales", k_scales, 2), ("v_scales", v_scales, 2),
-                        ("block_table", block_table, 2), ("seq_lens", seq_lens, 1),
-                        ("cu_q", cu_q, 1)):
-        if not isinstance(t, torch.Tensor) or t.dim() != nd:
+    try:
+        fine = (k_pages.dim() == 4 and k_scales.dim() == 2 and block_table.dim() == 2 and
+                seq_lens.dim() == 1 and cu_q.dim() == 1 and v_pages.shape == k_pages.shape and
+                v_scales.shape == k_scales.shape)
+    except AttributeError:
+        fine = False
+    if not fine:
+        for name, t, nd in (("k_pages", k_pages, 4), ("v_pages", v_pages, 4),
+                            ("k_scales", k_scales, 2), ("v_scales", v_scales, 2),
+                            ("block_table", block_table, 2), ("seq_lens", seq_lens, 1),
+                            ("cu_q", cu_q, 1)):
             _dims(t, name, nd)
-    shape, table = k_pages.shape, block_table.shape
-    num_pages, Hkv, page_size, d = shape
-    S = seq_lens.shape[0]
-    if v_pages.shape != shape:
-        raise ValueError("v_pages must match k_pages, [num_pages, Hkv, page_size, d]")
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+        if v_pages.shape != k_pages.shape:
+            raise ValueError("v_pages must match k_pages, [num_pages, Hkv, page_size, d]")
+    num_pages, Hkv, page_size, d = k_pages.shape
+    S, max_blocks = block_table.shape
+    if k_scales.shape != (num_pages, Hkv) or v_scales.shape != (num_pages, Hkv):
         raise ValueError("scales must be [num_pages, Hkv]")
-    if table[0] != S or cu_q.shape[0] != S + 1:
+    if seq_lens.numel() != S or cu_q.numel() != S + 1:
         raise ValueError("block_table needs S rows and cu_q S+1 entries")
-    return num_pages, Hkv, page_size, d, S, table[1]
+    return num_pages, Hkv, page_size, d, S, max_blocks
 
 
 def _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format,
-              device):
-    index = device.index
+              device, index):
     codes = _KV_DTYPES[kv_format]
+    f32, i32 = torch.float32, torch.int32
+    if (k_pages.dtype in codes and v_pages.dtype in codes and k_scales.dtype is f32 and
+            v_scales.dtype is f32 and block_table.dtype is i32 and seq_lens.dtype is i32 and
+            cu_q.dtype is i32 and k_pages.is_contiguous() and v_pages.is_contiguous() and
+            k_scales.is_contiguous() and v_scales.is_contiguous() and
+            block_table.is_contiguous() and seq_lens.is_contiguous() and cu_q.is_contiguous() and
+            index == k_pages.get_device() == v_pages.get_device() == k_scales.get_device() ==
+            v_scales.get_device() == block_table.get_device() == seq_lens.get_device() ==
+            cu_q.get_device()):
+        return
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
         if t.dtype not in codes:
             raise TypeError("%s must be one of %s for kv_format %r" % (name, codes, kv_format))
-        if not _is(t, t.dtype, 4, index):
-            _check(t, name, t.dtype, 4)
-            _same_device(device, **{name: t})
-    for name, t, dtype, nd in (("k_scales", k_scales, torch.float32, 2),
-                               ("v_scales", v_scales, torch.float32, 2),
-                               ("block_table", block_table, torch.int32, 2),
-                               ("seq_lens", seq_lens, torch.int32, 1),
-                               ("cu_q", cu_q, torch.int32, 1)):
-        if not _is(t, dtype, nd, index):
-            _check(t, name, dtype, nd)
-            _same_device(device, **{name: t})
+        _check(t, name, t.dtype, 4)
+    _check(k_scales, "k_scales", f32, 2)
+    _check(v_scales, "v_scales", f32, 2)
+    _check(block_table, "block_table", i32, 2)
+    _check(seq_lens, "seq_lens", i32, 1)
+    _check(cu_q, "cu_q", i32, 1)
+    _same_device(device, k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales,
+                 block_table=block_table, seq_lens=seq_lens, cu_q=cu_q)
+
+
+_kv_write, _kv_read, _prefill_q8 = (_Call("attn_kv_write_paged_q8"), _Call("attn_kv_read_paged_q8"),
+                                    _Call("attn_prefill_paged_q8"))
+_rope, _norm_rope, _norm_rope_bwd = (_Call("attn_rope"), _Call("attn_norm_rope"),
+                                     _Call("attn_norm_rope_bwd"))
 
 
 def attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
@@ -643,25 +665,25 @@ def attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_tab
     """
     num_pages, Hkv, page_size, d, S, max_blocks = _q8_cache(
         k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
-    for name, t in (("k", k), ("v", v)):
-        _dims(t, name, 3)
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.dim() == 3):
+        _dims(k, "k", 3)
+        _dims(v, "v", 3)
     T = k.shape[0]
     if k.shape != (T, Hkv, d) or v.shape != (T, Hkv, d):
         raise ValueError("k and v must be [T, Hkv, d] as the pages are")
     _rows(k, "k", torch.bfloat16)
     _rows(v, "v", torch.bfloat16)
-    device = k.device
-    _same_device(device, v=v)
-    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device)
+    device, index = k.device, k.get_device()
+    if v.get_device() != index:
+        _same_device(device, v=v)
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device,
+              index)
     kh, kt = _row_strides(k)
     vh, vt = _row_strides(v)
-    with _OnDevice(device.index):
-        rc = library().attn_kv_write_paged_q8(
-            k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, k_pages.data_ptr(), v_pages.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), KV_FORMATS[kv_format],
-            block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S, Hkv, T, int(max_q), d,
-            page_size, max_blocks, num_pages, _stream(k))
-    _raise(rc, "attn_kv_write_paged_q8")
+    _kv_write(index, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, k_pages.data_ptr(),
+              v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), KV_FORMATS[kv_format],
+              block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S, Hkv, T, int(max_q),
+              d, page_size, max_blocks, num_pages, _stream(k))
 
 
 def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
@@ -678,29 +700,28 @@ def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq
         k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
     if dtype not in _DTYPES:
         raise TypeError("dtype must be torch.bfloat16 or torch.float32")
-    shape = (int(tokens), Hkv, d)
+    T = int(tokens)
+    shape = (T, Hkv, d)
     for name, t in (("k", k), ("v", v)):
         if t is not None:
             _dims(t, name, 3)
-            if tuple(t.shape) != shape:
+            if t.shape != shape:
                 raise ValueError("k and v must be [tokens, Hkv, d]")
-    device = k_pages.device
-    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device)
+    device, index = k_pages.device, k_pages.get_device()
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device,
+              index)
     if k is None:
-        k = k_pages.new_empty(shape, dtype=dtype)
+        k = torch.empty(shape, dtype=dtype, device=device)
     if v is None:
-        v = k_pages.new_empty(shape, dtype=dtype)
-    for name, t in (("k", k), ("v", v)):
-        if not _is(t, dtype, 3, device.index):
-            _check(t, name, dtype, 3)
-            _same_device(device, **{name: t})
-    with _OnDevice(device.index):
-        rc = library().attn_kv_read_paged_q8(
-            k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-            KV_FORMATS[kv_format], block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
-            k.data_ptr(), v.data_ptr(), _DTYPES[dtype], S, Hkv, int(tokens), int(max_q), d,
-            page_size, max_blocks, num_pages, _stream(k_pages))
-    _raise(rc, "attn_kv_read_paged_q8")
+        v = torch.empty_like(k)
+    if not (_is(k, dtype, 3, index) and _is(v, dtype, 3, index)):
+        _check(k, "k", dtype, 3)
+        _check(v, "v", dtype, 3)
+        _same_device(device, k=k, v=v)
+    _kv_read(index, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+             v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
+             seq_lens.data_ptr(), cu_q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dtype], S,
+             Hkv, T, int(max_q), d, page_size, max_blocks, num_pages, _stream(k))
     return k, v
 
 
@@ -733,8 +754,9 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
         if alibi_slopes.numel() != Hq:
             raise ValueError("alibi_slopes needs one value per query head")
     _check(q, "q", torch.bfloat16, 3)
-    device = q.device
-    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device)
+    device, index = q.device, q.get_device()
+    _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format, device,
+              index)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out, lse = _decode_outputs(q, T, Hq, out, lse)
@@ -744,19 +766,16 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
         slopes_ptr = alibi_slopes.data_ptr()
     need = prefill_q8_workspace_bytes(S, Hq, Hkv, T, int(max_q), d, max_blocks, page_size)
     if workspace is None and need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     if workspace is not None:
         _check(workspace, "workspace", torch.uint8, 1)
     _same_device(device, out=out, lse=lse, alibi_slopes=alibi_slopes, workspace=workspace)
-    with _OnDevice(device.index):
-        rc = library().attn_prefill_paged_q8(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
-            seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Hq, Hkv, T,
-            int(max_q), d, page_size, max_blocks, num_pages, float(scale), int(window), slopes_ptr,
-            workspace.data_ptr() if workspace is not None else None,
-            workspace.numel() if workspace is not None else 0, _stream(q))
-    _raise(rc, "attn_prefill_paged_q8")
+    _prefill_q8(index, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
+                seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Hq, Hkv,
+                T, int(max_q), d, page_size, max_blocks, num_pages, float(scale), int(window),
+                slopes_ptr, workspace.data_ptr() if workspace is not None else None,
+                workspace.numel() if workspace is not None else 0, _stream(q))
     return out, lse
 
 
@@ -813,23 +832,17 @@ def _row_strides(t):
     return head if H > 1 else 0, token if T > 1 else 0
 
 
-def _strides(*tensors):
-    """The attn_strides_t of each tensor as addresses (None for None), and the array that holds
-    them: keep it until the call."""
-    flat, at = [], []
-    for t in tensors:
-        if t is None:
-            at.append(None)
-            continue
-        at.append(len(flat) * 8)
-        n, st = t.shape, t.stride()
-        if len(n) == 3:
-            flat += (0, st[1] if n[1] > 1 else 0, st[0] if n[0] > 1 else 0)
-        else:
-            flat += (st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0)
-    held = (ctypes.c_int64 * len(flat))(*flat)
-    base = ctypes.addressof(held)
-    return [None if a is None else base + a for a in at], held
+_three = struct.Struct("3q").pack  # an attn_strides_t
+
+
+def _strides(t):
+    """A tensor's attn_strides_t as bytes, which ctypes passes by address."""
+    if t is None:
+        return None
+    n, st = t.shape, t.stride()
+    if len(n) == 3:
+        return _three(0, st[1] if n[1] > 1 else 0, st[0] if n[0] > 1 else 0)
+    return _three(st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0)
 
 
 def _rope_args(q, k, positions, inv_freq, like_q, like_k):
@@ -870,21 +883,22 @@ def _rope_args(q, k, positions, inv_freq, like_q, like_k):
                 _dims(t, name, nd)
                 if t.shape != ref.shape:
                     raise ValueError("%s must have %s's shape" % (name, what))
-    dtype, device = q.dtype, q.device
+    dtype, index = q.dtype, q.get_device()
     if dtype not in _DTYPES:
         raise TypeError("q must be bfloat16 or float32, got %s" % dtype)
     _rows(q, "q", dtype)
     if k is not None:
         _rows(k, "k", dtype)
-        _same_device(device, k=k)
+        if k.get_device() != index:
+            _same_device(q.device, k=k)
     for name, t in like_q + like_k:
         if t is not None:
             _rows(t, name, dtype)
-            _same_device(device, **{name: t})
-    for name, t, dt in (("positions", positions, torch.int32), ("inv_freq", inv_freq, torch.float64)):
-        if not _is(t, dt, t.dim(), device.index):
-            _check(t, name, dt, t.dim())
-            _same_device(device, **{name: t})
+            _same_device(q.device, **{name: t})
+    if not (_is(positions, torch.int32, len(ps), index) and _is(inv_freq, torch.float64, 1, index)):
+        _check(positions, "positions", torch.int32, len(ps))
+        _check(inv_freq, "inv_freq", torch.float64, 1)
+        _same_device(q.device, positions=positions, inv_freq=inv_freq)
     return B, Hq, Hkv, N, d, N if len(ps) == 2 else 0
 
 
@@ -913,13 +927,10 @@ def attn_rope(q, k, positions, inv_freq, interleaved: bool = False, attention_fa
                                               [("k_out", k_out)])
     q_out = _empty_rows(q) if q_out is None else q_out
     k_out = _empty_rows(k) if k_out is None else k_out
-    st, held = _strides(q, q_out, k, k_out)
-    with _OnDevice(q.get_device()):
-        rc = library().attn_rope(_ptr(q), st[0], _ptr(q_out), st[1], _ptr(k), st[2], _ptr(k_out),
-                                 st[3], positions.data_ptr(), pos_stride, inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N, d,
-                                 2 * inv_freq.shape[0], int(bool(interleaved)),
-                                 float(attention_factor), int(bool(transpose)), _stream(q))
-    _raise(rc, "attn_rope")
+    _rope(q.get_device(), _ptr(q), _strides(q), _ptr(q_out), _strides(q_out), _ptr(k), _strides(k),
+          _ptr(k_out), _strides(k_out), positions.data_ptr(), pos_stride, inv_freq.data_ptr(),
+          _DTYPES[q.dtype], B, Hq, Hkv, N, d, 2 * inv_freq.shape[0], int(bool(interleaved)),
+          float(attention_factor), int(bool(transpose)), _stream(q))
     return q_out, k_out
 
 
@@ -949,15 +960,11 @@ def attn_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1
     _norm_weights(q, k, q_weight, k_weight)
     q_out = _empty_rows(q) if q_out is None else q_out
     k_out = _empty_rows(k) if k_out is None else k_out
-    st, held = _strides(q, q_out, k, k_out)
-    with _OnDevice(q.get_device()):
-        rc = library().attn_norm_rope(_ptr(q), st[0], _ptr(q_weight), _ptr(q_out), st[1], _ptr(k),
-                                      st[2], _ptr(k_weight), _ptr(k_out), st[3],
-                                      positions.data_ptr(), pos_stride, inv_freq.data_ptr(),
-                                      _DTYPES[q.dtype], B, Hq, Hkv, N, d, 2 * inv_freq.shape[0],
-                                      int(bool(interleaved)), float(attention_factor), float(eps),
-                                      _stream(q))
-    _raise(rc, "attn_norm_rope")
+    _norm_rope(q.get_device(), _ptr(q), _strides(q), _ptr(q_weight), _ptr(q_out), _strides(q_out),
+               _ptr(k), _strides(k), _ptr(k_weight), _ptr(k_out), _strides(k_out),
+               positions.data_ptr(), pos_stride, inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv,
+               N, d, 2 * inv_freq.shape[0], int(bool(interleaved)), float(attention_factor),
+               float(eps), _stream(q))
     return q_out, k_out
 
 
@@ -995,24 +1002,22 @@ def attn_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, positions, inv_
     dq = _empty_rows(q) if dq is None else dq
     dk = _empty_rows(k) if dk is None else dk
     if dq_weight is None:
-        dq_weight = q.new_empty(d, dtype=torch.float32)
+        dq_weight = torch.empty(d, dtype=torch.float32, device=q.device)
     if dk_weight is None and k is not None:
-        dk_weight = q.new_empty(d, dtype=torch.float32)
+        dk_weight = torch.empty_like(dq_weight)
     if workspace is None:
         need = norm_rope_bwd_workspace_bytes(B, Hq, Hkv, N, d)
-        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     elif not _is(workspace, torch.uint8, 1, index):
         _check(workspace, "workspace", torch.uint8, 1)
         _same_device(q.device, workspace=workspace)
-    st, held = _strides(q, dq_out, dq, k, dk_out, dk)
-    with _OnDevice(index):
-        rc = library().attn_norm_rope_bwd(
-            _ptr(q), st[0], _ptr(q_weight), _ptr(dq_out), st[1], _ptr(dq), st[2], _ptr(dq_weight),
-            _ptr(k), st[3], _ptr(k_weight), _ptr(dk_out), st[4], _ptr(dk), st[5], _ptr(dk_weight),
-            positions.data_ptr(), pos_stride, inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq, Hkv, N,
-            d, 2 * inv_freq.shape[0], int(bool(interleaved)), float(attention_factor), float(eps),
-            workspace.data_ptr(), workspace.numel(), _stream(q))
-    _raise(rc, "attn_norm_rope_bwd")
+    _norm_rope_bwd(index, _ptr(q), _strides(q), _ptr(q_weight), _ptr(dq_out), _strides(dq_out),
+                   _ptr(dq), _strides(dq), _ptr(dq_weight), _ptr(k), _strides(k), _ptr(k_weight),
+                   _ptr(dk_out), _strides(dk_out), _ptr(dk), _strides(dk), _ptr(dk_weight),
+                   positions.data_ptr(), pos_stride, inv_freq.data_ptr(), _DTYPES[q.dtype], B, Hq,
+                   Hkv, N, d, 2 * inv_freq.shape[0], int(bool(interleaved)),
+                   float(attention_factor), float(eps), workspace.data_ptr(), workspace.numel(),
+                   _stream(q))
     return dq, dk, dq_weight, dk_weight
 
 
