@@ -204,7 +204,8 @@ def _same_device(device, **tensors):
 def _is(t, dtype, ndim: int, index: int) -> bool:
     """Whether a tensor is a dense one of this type and rank on this GPU: what _check and
     _same_device ask, in a few attribute reads (they name what is wrong where it is not)."""
-    return (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and t.get_device() == index)
+    return (t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and
+            t.get_device() == index >= 0)  # (-1: not on a GPU)
 
 
 class _Call:
@@ -212,17 +213,15 @@ class _Call:
     where another is) and its error raised."""
 
     def __init__(self, name: str):
-        self.name, self.fn = name, None
+        self.name = name
 
     def __call__(self, index: int, *args):
-        if self.fn is None:
-            self.fn = getattr(library(), self.name)
-        back = torch._C._cuda_getDevice()
-        if back == index:
-            rc = self.fn(*args)
+        fn = getattr(library(), self.name)
+        if torch._C._cuda_getDevice() == index:
+            rc = fn(*args)
         else:
             with torch.cuda.device(index):
-                rc = self.fn(*args)
+                rc = fn(*args)
         if rc != 0:
             raise AttnError(rc, self.name)
 
@@ -627,7 +626,7 @@ def _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
             cu_q.dtype is i32 and k_pages.is_contiguous() and v_pages.is_contiguous() and
             k_scales.is_contiguous() and v_scales.is_contiguous() and
             block_table.is_contiguous() and seq_lens.is_contiguous() and cu_q.is_contiguous() and
-            index == k_pages.get_device() == v_pages.get_device() == k_scales.get_device() ==
+            0 <= index == k_pages.get_device() == v_pages.get_device() == k_scales.get_device() ==
             v_scales.get_device() == block_table.get_device() == seq_lens.get_device() ==
             cu_q.get_device()):
         return

@@ -100,6 +100,69 @@ def test_not_split(fmt):
     check(*run(on_gpu(st), fmt), reference(st, fmt))
 
 
+# The ways a call is cut: chunks that fit one row tile of 128 rows (twin tiles over
+# halves of the keys) or not, as many work items as SMs or fewer (keys split over
+# CTAs, by each sequence's length), one key tile for all.
+@pytest.mark.parametrize("qlens,ctxs,Hq,Hkv,d,split", [
+    ([4, 1, 4], [3000, 100, 1290], 8, 2, 128, True),          # twin, split
+    ([1], [9000], 4, 1, 64, True),                            # one work item over all SMs
+    ([32, 31], [1000, 127], 8, 2, 64, True),                  # a full tile of rows
+    ([33, 20, 1], [1500, 900, 2600], 8, 2, 64, True),         # one row tile and a bit: not twin
+    ([140], [2000], 4, 2, 128, True),                         # three tiles, the keys split
+    ([2] * 40, [37 * i for i in range(40)], 8, 4, 64, False),         # twin, enough work items
+    ([50] * 40, [150 + 11 * i for i in range(40)], 8, 4, 64, False),  # neither
+    ([0] * 30 + [3] + [0] * 40, [500] * 71, 2, 2, 64, True),  # most sequences have no chunk
+])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_every_cut(qlens, ctxs, Hq, Hkv, d, split, fmt):
+    st = make(qlens, ctxs, Hq, Hkv, d, fmt, seed=len(qlens) + d)
+    need = ea.prefill_q8_workspace_bytes(len(qlens), Hq, Hkv, sum(qlens), max(qlens), d, st["block_table"].shape[1])
+    assert (need > 0) == split
+    dv = on_gpu(st)
+    ws = torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV)  # NaN wherever nothing is written
+    check(*run(dv, fmt, workspace=ws), reference(st, fmt))
+    # A table far wider than the lengths cuts the call otherwise; so does a larger bound.
+    wide = torch.full((len(qlens), dv["block_table"].shape[1] + 300), -1, dtype=torch.int32, device=DEV)
+    wide[:, :dv["block_table"].shape[1]] = dv["block_table"]
+    dv["block_table"] = wide
+    check(*run(dv, fmt, max_q=max(qlens) + 70), reference(st, fmt))
+    assert ea.device_status() == 0
+
+
+def test_many_splits_join():
+    # Long keys whose parts differ by far in weight: the last keys' scores dominate.
+    st = make([3], [6000], 4, 1, 128, "e4m3", seed=19)
+    st["k_scales"] *= torch.linspace(0.2, 3.0, st["k_scales"].shape[0])[:, None]
+    check(*run(on_gpu(st), "e4m3"), reference(st, "e4m3"), wide=2.0 ** -12)
+
+
+@pytest.mark.parametrize("window", [0, 40, 500])
+@pytest.mark.parametrize("qlen,copies", [(5, 0), (5, 80), (90, 0), (90, 80)])
+def test_nan_scale_reaches_its_rows_only(window, qlen, copies):
+    # Twin tiles and others, split keys and not: a page whose V scale is NaN, in the tile of the
+    # diagonal and in an earlier one.
+    ctx = 700
+    st = make([qlen] + [1] * copies, [ctx] + [200] * copies, 4, 2, 64, "int8", seed=23)
+    want = reference(st, "int8", window=window)
+    for tok in (ctx, 300):
+        sick = dict(st, v_scales=st["v_scales"].clone())
+        sick["v_scales"][int(st["block_table"][0, tok // 16]), 1] = float("nan")
+        o, lse = run(on_gpu(sick), "int8", window=window)
+        pos = ctx + np.arange(qlen)
+        page = tok // 16 * 16
+        hit = pos >= page
+        if window:
+            hit &= pos - window + 1 <= page + 15
+        rows = np.zeros((qlen + copies, 4), bool)
+        rows[:qlen, 2:] = hit[:, None]
+        assert o[torch.from_numpy(rows).to(DEV)].isnan().all()
+        assert lse.isfinite().all()
+        keep = ~rows
+        got = f64(o)[keep]
+        lim = 2.0 ** -8 * np.abs(want[0][keep]) + 2.0 ** -9.7 * want[2][keep] + 1e-30
+        assert (np.abs(got - want[0][keep]) <= lim).all()
+
+
 def test_more_sequences_than_are_ranked():
     qlens, ctxs = [1] * 600, [i % 23 for i in range(600)]
     st = make(qlens, ctxs, 2, 1, 64, "int8", seed=4)
@@ -230,6 +293,32 @@ def test_bad_pages_and_lengths():
         assert ea.device_status(clear=True) == ea.ATTN_DEV_BAD_PAGE
         assert (o[10:20] == 3).all()
         check(o[keep], lse[keep], tuple(x[keep] for x in want))
+
+
+def test_waits_run_out():
+    """The library's test build stops the copies early: the kernels' waits run out, the call
+    returns and the status says so; the product library then works on the same device."""
+    from exact_io_aware_101_b200 import build as eabuild
+    import ctypes
+    tlib = ea.load_library(eabuild.build_test_lib())
+    for qlens, ctxs in (([4, 4], [700, 900]), ([100], [900]), ([4] * 80, [300] * 80)):
+        st = make(qlens, ctxs, 4, 2, 128, "e4m3", seed=17)
+        dv = on_gpu(st)
+        T, mb, P = sum(qlens), dv["block_table"].shape[1], dv["k_pages"].shape[0]
+        need = ea.prefill_q8_workspace_bytes(len(qlens), 4, 2, T, max(qlens), 128, mb)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        o, lse = torch.empty_like(dv["q"]), torch.empty(T, 4, device=DEV)
+        rc = tlib.attn_prefill_paged_q8(
+            dv["q"].data_ptr(), *(dv[n].data_ptr() for n in CACHE[:4]), 0, *(dv[n].data_ptr() for n in CACHE[4:]),
+            o.data_ptr(), lse.data_ptr(), len(qlens), 4, 2, T, max(qlens), 128, 16, mb, P, 128 ** -0.5, 0, None,
+            ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        word = ctypes.c_uint(0)
+        assert tlib.attn_device_status(ctypes.byref(word), 1, torch.cuda.current_stream().cuda_stream) == 0
+        assert word.value == ea.ATTN_DEV_TIMEOUT
+        check(*run(dv, "e4m3"), reference(st, "e4m3"))
+    assert ea.device_status() == 0
 
 
 def test_large_query_values():
