@@ -29,12 +29,12 @@
 //  * Exactness.  Codes are exact in f16.  Queries are scaled by a power of two
 //    per row before rounding to f16, exact for elements within 2^28 of the
 //    row's largest.  The K scale multiplies the f32 scores, per page.  The V
-//    scale, relative to a power of two just above the largest V scale of the
-//    CTA's pages, multiplies the code on its way to f16, rounded once: v =
-//    fma(code, hi, code * lo) with hi + lo the scale to 22 bits; or (twin tiles)
-//    P before it is rounded to f16.  (A page whose V scale is under 2^-19 of that
-//    largest one loses bits of its own values.)  P is rounded to f16 (2^-11 of
-//    each, against bf16's 2^-8 of the output).
+//    scale, relative to a power of two below the largest V scale of the CTA's
+//    pages, multiplies P in f32 before it is rounded to f16 (2^-11 of each,
+//    against bf16's 2^-8 of the output).  (Terms under 2^-19 of the largest V
+//    scale times the row's largest P lose bits.  Scaling the codes on their way
+//    instead costs two roundings, and as much time: 600 us for the 16 chunks
+//    either way, in a run long enough for the power limit.)
 //  * Few rows and long keys: when the row tiles alone leave SMs idle, each
 //    tile's keys are split over several CTAs, which write normalised partials
 //    and their log2-sum-exps to the workspace; a second kernel, scheduled
@@ -61,7 +61,7 @@ constexpr int BN = 128;  // keys of a tile
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = BN / kPage;
 constexpr int NUM_THREADS = 512;
-constexpr int kRegsMma = 88, kRegsWiden = 104, kRegsSoft = 160;
+constexpr int kRegsMma = 88, kRegsWiden = 88, kRegsSoft = 168;
 static_assert(128 * (kRegsMma + kRegsWiden + 2 * kRegsSoft) <= NUM_THREADS * 128,
               "setmaxnreg split must fit the block's launch registers");
 constexpr int kRankMax = NUM_THREADS;   // sequences ranked by length
@@ -104,7 +104,7 @@ struct Shared {
   uint64_t mma_done;
   alignas(16) float k_scale[kScaleRing][kPagesPerTile];
   alignas(16) float v_scale[kScaleRing][kPagesPerTile];
-  unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with a NaN or infinite value
+  unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with a code that is no number
   unsigned v_top;                      // largest finite |V scale| of the CTA's pages, as bits
   int any_bad;
   unsigned poison1[BM / 32];  // twin: rows of tile 1 that see a value left out
@@ -181,9 +181,8 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &a, uint32_t &b) {
 }
 
 // Half a score row (64 columns, four pages) -> 32 f16 pairs of P = 2^(s*c - m), c
-// the multiplier of the columns' page, and (kScaled) times their pages' V scale v;
-// returns the part of the row sum, which has no V scale.
-template <bool kScaled>
+// the multiplier of the columns' page, times their page's V scale v; returns the
+// part of the row sum, which has no V scale.
 __device__ __forceinline__ float exp_half(const uint32_t (&sv)[64], const float *c, const float *v,
                                           float m, uint32_t (&pk)[32]) {
   const float2 nm2 = make_float2(-m, -m);
@@ -197,11 +196,9 @@ __device__ __forceinline__ float exp_half(const uint32_t (&sv)[64], const float 
     float2 p1 = make_float2(ex2(x1.x), ex2(x1.y));
     sum_a = add2(sum_a, p0);
     sum_b = add2(sum_b, p1);
-    if constexpr (kScaled) {
-      const float2 v2 = make_float2(v[i / kPage], v[i / kPage]), z2 = make_float2(0.f, 0.f);
-      p0 = fma2(p0, v2, z2);
-      p1 = fma2(p1, v2, z2);
-    }
+    const float2 v2 = make_float2(v[i / kPage], v[i / kPage]), z2 = make_float2(0.f, 0.f);
+    p0 = fma2(p0, v2, z2);
+    p1 = fma2(p1, v2, z2);
     pk[i >> 1] = pack_f16x2(p0.x, p0.y);
     pk[(i >> 1) + 1] = pack_f16x2(p1.x, p1.y);
   }
@@ -627,8 +624,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         const int pg = j * kPagesPerTile + u;
         return pg * kPage < ck.n ? table[pg] : -1;
       };
-      // The scale of its tensor; twin tiles take both with K, since the softmax
-      // applies V's.
+      // Both scales, with K: the softmax applies them.
       auto scale_of = [&](int i, int pid) {
         bool v;
         int j, slot;
@@ -637,7 +633,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         entry<kTwin>(i + e, jlo, total, v, j, slot);
         const size_t slice = static_cast<size_t>(pid) * p.Hkv + hkv;
         if (!v) x.x = p.k_scales[slice];
-        if (kTwin ? !v : v) x.y = p.v_scales[slice] * v_unit;
+        if (!v) x.y = p.v_scales[slice] * v_unit;
         return x;
       };
       int issued = 0;
@@ -665,9 +661,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           entry<kTwin>(i, jlo, total, v, j, scale_slot);
           // (A scale slot comes round after eight tiles; the rings hold at most six
           // between here and the softmax.)
-          if (e == k) {
-            if (!v) sh->k_scale[scale_slot][u] = scale.x;
-            if (kTwin ? !v : v) sh->v_scale[scale_slot][u] = scale.y;
+          if (!v && e == k) {
+            sh->k_scale[scale_slot][u] = scale.x;
+            sh->v_scale[scale_slot][u] = scale.y;
           }
           __syncwarp();
           if (lane == 0)
@@ -715,7 +711,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     // before it (900 cycles a tile); twin tiles, where this is what bounds the
     // kernel, load all of it first (700; beside two busy softmaxes that gains
     // nothing: 560 us against 549 for 16 chunks of 512).
-    auto widen_plain = [&](const uint8_t *src, uint8_t *dst) {
+    auto widen = [&](const uint8_t *src, uint8_t *dst) {
       constexpr int A = kTwin ? 2 * PASSES : 1;
 #pragma unroll
       for (int u0 = 0; u0 < 2 * PASSES; u0 += A) {
@@ -743,48 +739,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       mbar_arrive(&sh->full[i % C::NST]);
       mbar_arrive(&sh->raw_empty[i % C::NRAW]);
     };
-    auto widen_k = [&](int i) {
-      if (!ready(i)) return false;
-      const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
+    for (int i = 0; i < total; ++i) {
+      bool v;
+      int j, scale_slot;
+      entry<kTwin>(i, jlo, total, v, j, scale_slot);
+      if (!ready(i)) break;
       uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
-      widen_plain(src, dst);
-      done(i);
-      return true;
-    };
-    auto widen_v = [&](int i, int j, int scale_slot) {
-      if (!ready(i)) return false;
-      const uint8_t *src = smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from;
-      uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
-      // Tiles that some row sees only in part: their slot in v_bad, or -1.
-      const int edge = j >= edge_hi ? min(j - edge_hi, kEdge - 1)
-                                    : (p.window > 0 && j - edge_0 < kEdge ? kEdge + j - edge_0 : -1);
-      if constexpr (kTwin) {
-        widen_plain(src, dst);
-      } else {
-        const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[scale_slot][2 * w]);
-#pragma unroll
-        for (int u = 0; u < 2 * PASSES; ++u) {
-          const float s = u < PASSES ? vs.x : vs.y;
-          const __half hi = __float2half_rn(s);
-          const __half lo = __float2half_rn(s - __half2float(hi));
-          const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(lo);
-          const uint4 c = *reinterpret_cast<const uint4 *>(src + u * 512);
-          uint32_t f[8];
-          widen4<FMT>(c.x, f[0], f[1]);
-          widen4<FMT>(c.y, f[2], f[3]);
-          widen4<FMT>(c.z, f[4], f[5]);
-          widen4<FMT>(c.w, f[6], f[7]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __half2 x = as_h2(f[e]);
-            f[e] = as_u32(__hfma2(x, hi2, __hmul2(x, lo2)));
-          }
-          put(dst, 2 * w * kPage + u * RPP + row, make_uint4(f[0], f[1], f[2], f[3]),
-              make_uint4(f[4], f[5], f[6], f[7]));
-        }
-      }
+      widen(smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from, dst);
+      // V tiles that some row sees only in part: their slot in v_bad, or -1.  (An
+      // INT8 code is always a number.)
+      const int edge = FMT != ATTN_KV_E4M3 || !v ? -1
+                       : j >= edge_hi            ? min(j - edge_hi, kEdge - 1)
+                       : p.window > 0 && j - edge_0 < kEdge ? kEdge + j - edge_0 : -1;
       if (edge >= 0) {
-        // What this lane stored, again: values that are no numbers leave.
+        // What this lane stored, again: codes that are no numbers leave.
 #pragma unroll 1
         for (int u = 0; u < 2 * PASSES; ++u) {
           const int r = 2 * w * kPage + u * RPP + row;
@@ -807,20 +775,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         }
       }
       done(i);
-      return true;
-    };
-    for (int i = 0; i < total; i += 2) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        bool v;
-        int j, scale_slot;
-        entry<kTwin>(i + k, jlo, total, v, j, scale_slot);
-        // (Without twins every other entry is a V, known when compiling.)
-        if (!((kTwin ? v : k == 1) ? widen_v(i + k, j, scale_slot) : widen_k(i + k))) {
-          i = total;
-          break;
-        }
-      }
     }
   } else {
     // ====================================================== softmax / epilogue
@@ -903,10 +857,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         cp[0] = a.x * c_row; cp[1] = a.y * c_row; cp[2] = a.z * c_row; cp[3] = a.w * c_row;
         cp[4] = b.x * c_row; cp[5] = b.y * c_row; cp[6] = b.z * c_row; cp[7] = b.w * c_row;
       }
-      // Twin tiles: the V scales, which P takes here.
-      float vp[kTwin ? kPagesPerTile : 1];
-      if constexpr (kTwin) {
-        const float4 *vs = reinterpret_cast<const float4 *>(sh->v_scale[(2 * jj + t) % kScaleRing]);
+      // The V scales, which P takes here.
+      float vp[kPagesPerTile];
+      {
+        const float4 *vs = reinterpret_cast<const float4 *>(sh->v_scale[(kTwin ? 2 * jj + t : j - jlo) % kScaleRing]);
         const float4 a = vs[0], b = vs[1];
         vp[0] = a.x; vp[1] = a.y; vp[2] = a.z; vp[3] = a.w;
         vp[4] = b.x; vp[5] = b.y; vp[6] = b.z; vp[7] = b.w;
@@ -934,7 +888,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         // max-first step below would have kept the reference too.
         tmem_ld64(s_addr, sv);
         tmem_ld_wait64(sv);
-        const float l0 = exp_half<kTwin>(sv, cp, vp, m, pk);
+        const float l0 = exp_half(sv, cp, vp, m, pk);
         if (__all_sync(0xffffffffu, l0 <= 255.0f)) {
           first_done = true;
           tmem_ld64(s_addr + 64, sv);
@@ -944,7 +898,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           mbar_arrive(&sh->p_half[t]);
           l += l0;
           tmem_ld_wait64(sv);
-          const float l1 = exp_half<kTwin>(sv, cp + 4, vp + (kTwin ? 4 : 0), m, pk);
+          const float l1 = exp_half(sv, cp + 4, vp + 4, m, pk);
           if (__all_sync(0xffffffffu, l1 <= 255.0f)) {
             l += l1;
             store_half(s_addr + 32, pk);
@@ -1021,12 +975,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
 #pragma unroll 1
       for (int h = first_done; h < 2; ++h) {
         scaled_half(h);
-        float vh[4];
-        if constexpr (kTwin) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vh[i] = h ? vp[4 + i] : vp[i];
-        }
-        l += exp_half<kTwin>(sv, ones, vh, m_use, pk);
+        const float vh[4] = {h ? vp[4] : vp[0], h ? vp[5] : vp[1], h ? vp[6] : vp[2], h ? vp[7] : vp[3]};
+        l += exp_half(sv, ones, vh, m_use, pk);
         store_half(s_addr + 32 * h, pk);
         tmem_st_wait();
         tc_fence_before();
