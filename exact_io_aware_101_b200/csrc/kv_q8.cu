@@ -14,14 +14,20 @@
 // whose new tokens hold a NaN or an infinity gets the scale NaN: the sequence's
 // attention then is NaN, as it would be over a 16-bit cache.
 //
-// Exact quotients: each product with 1 / s' is corrected by its remainder, whose
-// sign then decides the rounding (see codes8), for every element alike.  bf16
-// values meet ties often: x = amax / 2 is 63.5 steps of INT8 but for the scale's
-// own rounding, and every power of two times 3/4 amax may lie half way between
-// two E4M3 codes.  (Two products that enclose the quotient, and a division in 64
-// bits where they round apart, took 24 us (INT8) and 36 us (E4M3) for 16 chunks
-// of 512 tokens of 8 heads, d = 128; the remainder where they round apart as long
-// as the remainder everywhere, 17 and 18 us.)
+// Exact quotients.  bf16 values meet ties often: x = amax / 2 is 63.5 steps of INT8
+// but for the scale's own rounding, and every power of two times 3/4 amax may lie
+// half way between two E4M3 codes.  Two ways, chosen for a slice as a whole:
+//  * s' is the rounded amax / qmax of these very tokens, and not exact.  x and amax
+//    have 8 bits, qmax and a tie t at most 8: x qmax and t amax, whole numbers but
+//    for powers of two, are equal or at least 2^-16 apart.  Where they are equal
+//    the quotient lies on the side of the tie that the rounding of s' put it on,
+//    one side for all elements.  So one product with 1 / s', moved by 2^-22 to
+//    that side (more than its own errors, far less than 2^-16), rounds right.
+//  * Otherwise (an earlier scale stays, amax / qmax is exact, a rescaled code) each
+//    quotient's remainder decides (see codes8).
+// (For 16 chunks of 512 tokens of 8 heads, d = 128: a division in 64 bits near ties
+// took 24 us (INT8) and 36 us (E4M3), the remainder for every element 17 and 18,
+// five integer operations an element, the integer unit the busiest.)
 //
 // What bounds it: HBM for long chunks and for reading, one chain of dependent
 // loads (lengths, block table, data) for a decode step.  One warp takes one
@@ -160,6 +166,19 @@ __device__ __forceinline__ bool chunk_of(const int *seq_lens, const int *cu_q, i
          c.n <= static_cast<long long>(max_blocks) * kPage;
 }
 
+// Eight codes of x * f, f one product's factor.
+template <int FMT>
+__device__ __forceinline__ uint2 codes8_by_product(const float (&x)[8], float f) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 y = fma2(make_float2(x[i], x[i + 1]), make_float2(f, f), make_float2(0.f, 0.f));
+    q[i] = y.x;
+    q[i + 1] = y.y;
+  }
+  return make_uint2(codes4<FMT>(q), codes4<FMT>(q + 4));
+}
+
 struct WriteParams {
   const void *x[2];            // k, v (bf16)
   long long xt[2], xh[2];      // their token and head strides
@@ -230,12 +249,19 @@ __global__ void __launch_bounds__(kWarps * 32, 6) kv_write_kernel(const WritePar
   }
   uint32_t top = *reinterpret_cast<const uint32_t *>(&most) & 0x7fff7fffu;
   top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-  float s_new = fmaxf(__uint_as_float(top << 16) / kQmax, 1.17549435e-38f);
+  const float amax = __uint_as_float(top << 16);
+  const float s_own = amax / kQmax;
+  float s_new = fmaxf(s_own, 1.17549435e-38f);
   const bool odd = top >= 0x7f80u || !(fabsf(s_old) <= 3.4028235e38f);  // a NaN or infinity
   if (lo > 0) s_new = fmaxf(s_new, s_old);
   if (odd) s_new = __uint_as_float(0x7fc00000u);
   if (lane == 0) p.scales[kv][slice] = s_new;
 
+  // On which side of amax / qmax its rounding put the scale (exact: a multiple of
+  // the scale's last bit, of 8 bits at most).
+  const float left = fmaf(-s_new, kQmax, amax);
+  const bool by_product = s_new == s_own && left != 0.f;
+  const float factor = (1.f / s_new) * (left > 0.f ? 1.f + 0x1p-22f : 1.f - 0x1p-22f);
   const bool again = lo > 0 && s_new != s_old && !odd;
   const Divide by(1.f, odd ? 1.f : s_new), rescale(again ? s_old : 0.f, odd ? 1.f : s_new);
 #pragma unroll
@@ -250,7 +276,8 @@ __global__ void __launch_bounds__(kWarps * 32, 6) kv_write_kernel(const WritePar
         v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
       }
       *reinterpret_cast<uint2 *>(codes + r * D) =
-          odd ? make_uint2(0, 0) : codes8<FMT, false>(v, by);
+          odd ? make_uint2(0, 0)
+              : (by_product ? codes8_by_product<FMT>(v, factor) : codes8<FMT, false>(v, by));
     } else if (r < lo && again) {
       values4<FMT>(was[i].x, v);
       values4<FMT>(was[i].y, v + 4);

@@ -148,6 +148,25 @@ def test_write_ties(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_write_every_pair_of_mantissas(fmt):
+    # A slice for every 8-bit mantissa of its largest value, holding every mantissa at 16
+    # exponents: all the ties that bf16 values can meet, and how the scale's rounding breaks them.
+    d, n = 128, 128
+    amax = torch.arange(128, 256, dtype=torch.float64)
+    x = torch.arange(128, 256, dtype=torch.float64)[None, :] * torch.exp2(-torch.arange(1, 17, dtype=torch.float64))[:, None]
+    x = x[None].repeat(n, 1, 1)                      # [slice, 16 tokens, d]
+    x[:, 0, 0] = amax
+    x[:, 1::2] *= -1
+    for mul in (1.0, 2.0 ** 60, 2.0 ** -90):
+        st = make([16 * n], [0], 1, d, fmt, seed=1)
+        st["k"] = st["v"] = (x * mul).view(16 * n, 1, d).to(torch.bfloat16)
+        assert torch.equal(st["k"].double(), (x * mul).view(16 * n, 1, d))
+        dv = on_gpu(st)
+        write(dv, fmt)
+        check_written(st, dv, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_write_small_large_zero_and_not_numbers(fmt):
     st = make([16] * 7, [0] * 7, 2, 64, fmt, seed=5)
     for name in ("k", "v"):
