@@ -17,9 +17,8 @@
 //    group, and a chunk of a few tokens fills a tile instead of G of them.
 //  * 16 warps in four warpgroups:
 //      warp 0       allocates TMEM and issues every tcgen05.mma;
-//      warp 1       brings the codes of each 128-key tile to shared memory, one
-//                   untiled bulk copy per page (its slice is contiguous);
-//      warps 4-7    widen: each takes two pages of a tile, converts their codes
+//      warps 4-7    widen: each takes two pages of every 128-key tile, copies
+//                   their codes to shared memory three tiles ahead, converts them
 //                   and stores them into a ring of NST slots in the
 //                   128-byte-swizzled layout that the MMAs read;
 //      warps 8-11   softmax, correction and epilogue of tile 0, warps 12-15 of
@@ -61,9 +60,13 @@ constexpr int BN = 128;  // keys of a tile
 constexpr int kPage = 16;
 constexpr int kPagesPerTile = BN / kPage;
 constexpr int NUM_THREADS = 512;
-constexpr int kRegsMma = 88, kRegsWiden = 88, kRegsSoft = 168;
-static_assert(128 * (kRegsMma + kRegsWiden + 2 * kRegsSoft) <= NUM_THREADS * 128,
-              "setmaxnreg split must fit the block's launch registers");
+// Registers a thread by role; the widening of twin tiles holds a whole raw tile.
+template <bool kTwin>
+struct Regs {
+  static constexpr int kMma = kTwin ? 64 : 88, kWiden = kTwin ? 104 : 88, kSoft = 168;
+  static_assert(128 * (kMma + kWiden + 2 * kSoft) <= NUM_THREADS * 128,
+                "setmaxnreg split must fit the block's launch registers");
+};
 constexpr int kRankMax = NUM_THREADS;   // sequences ranked by length
 constexpr int CHUNK_BYTES = 128 * 128;  // one 128-row x 128-byte swizzle column block
 constexpr int kSMs = 148;
@@ -90,8 +93,6 @@ struct Cfg {
 };
 
 struct Shared {
-  uint64_t raw_full[4];
-  uint64_t raw_empty[4];
   uint64_t full[8];
   uint64_t empty[8];
   uint64_t q_full[2];
@@ -149,6 +150,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ __half2 as_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+// 16 bytes from global to shared memory behind this thread's back, or zeros where
+// `size` is 0; a group of them is closed, and waited for but for the N newest.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src, int size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A barrier of the softmax warps alone.
+__device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -180,15 +193,16 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &a, uint32_t &b) {
   }
 }
 
-// Half a score row (64 columns, four pages) -> 32 f16 pairs of P = 2^(s*c - m), c
+// N columns of a score row -> N / 2 f16 pairs of P = 2^(s*c - m), c
 // the multiplier of the columns' page, times their page's V scale v; returns the
 // part of the row sum, which has no V scale.
-__device__ __forceinline__ float exp_half(const uint32_t (&sv)[64], const float *c, const float *v,
-                                          float m, uint32_t (&pk)[32]) {
+template <int N>
+__device__ __forceinline__ float exp_cols(const uint32_t (&sv)[N], const float *c, const float *v,
+                                          float m, uint32_t (&pk)[N / 2]) {
   const float2 nm2 = make_float2(-m, -m);
   float2 sum_a = make_float2(0.f, 0.f), sum_b = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < 64; i += 4) {
+  for (int i = 0; i < N; i += 4) {
     const float2 c2 = make_float2(c[i / kPage], c[i / kPage]);
     const float2 x0 = fma2(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), c2, nm2);
     const float2 x1 = fma2(make_float2(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), c2, nm2);
@@ -410,13 +424,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     je1 = jhi;
   }
   const int total = 2 * (jhi - jlo);  // K and V tiles of the walk
+  // Twin tiles with at most a warp of rows: every quarter of a tile's lanes holds
+  // all of them, and takes a quarter of its columns.
+  const int rows_here = min(p.span, ck.nq - tok0) * p.heads;
+  const bool few = kTwin && rows_here <= 32;
 
   // ---- every page of those tiles must be in the pool; and their largest V scale.
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NRAW; ++i) {
-      mbar_init(&sh->raw_full[i], 1);
-      mbar_init(&sh->raw_empty[i], 128);
-    }
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&sh->full[i], 128);
       mbar_init(&sh->empty[i], 1);
@@ -489,7 +503,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
 
   if (warp < 4) {
     // ================================================================== MMA
-    regs_dec<kRegsMma>();
+    regs_dec<Regs<kTwin>::kMma>();
     if (warp == 0) {
       // The whole warp walks the schedule and one elected lane issues: with the
       // control flow uniform, the descriptors stay in uniform registers.  (One
@@ -605,88 +619,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       // Every MMA issued above must finish before TMEM is released.
       if (one) tc_commit(&sh->mma_done);
       mbar_wait_drain(&sh->mma_done, 0, p.status);
-    } else if (warp == 1) {
-      // =============================================================== copies
-      // Lane 8e + u brings page u of every fourth entry e, one untiled copy, and
-      // its scale.  Page numbers are read two rounds of four entries ahead and
-      // scales one, so that neither's latency is waited for (read an entry ahead,
-      // they held the copies to 2.4 TB/s).  Slots behind the keys keep what they
-      // held: their scores are masked, and the widening of such a tile lets no
-      // value that is no number pass.
-      const int *table = p.block_table + static_cast<size_t>(seq) * p.max_blocks;
-      const int u = lane & 7, e = lane >> 3;
-      const float v_unit = __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23);
-      auto page_of = [&](int i) {  // of this lane's entry of the round from i on
-        bool v;
-        int j, slot;
-        if (i + e >= total) return -1;
-        entry<kTwin>(i + e, jlo, total, v, j, slot);
-        const int pg = j * kPagesPerTile + u;
-        return pg * kPage < ck.n ? table[pg] : -1;
-      };
-      // Both scales, with K: the softmax applies them.
-      auto scale_of = [&](int i, int pid) {
-        bool v;
-        int j, slot;
-        float2 x = make_float2(0.f, 0.f);
-        if (pid < 0) return x;
-        entry<kTwin>(i + e, jlo, total, v, j, slot);
-        const size_t slice = static_cast<size_t>(pid) * p.Hkv + hkv;
-        if (!v) x.x = p.k_scales[slice];
-        if (!v) x.y = p.v_scales[slice] * v_unit;
-        return x;
-      };
-      int issued = 0;
-      bool go = true;
-      int pid = page_of(0), pid1 = page_of(4);
-      float2 scale = scale_of(0, pid);
-      for (int i0 = 0; go && i0 < total; i0 += 4) {
-        const float2 scale1 = scale_of(i0 + 4, pid1);
-        const int pid2 = page_of(i0 + 8);
-        const unsigned live = __ballot_sync(0xffffffffu, pid >= 0);
-#pragma unroll 1
-        for (int k = 0; k < 4 && i0 + k < total; ++k) {
-          const int i = i0 + k, slot = i % C::NRAW;
-          if (lane == 0 && i >= C::NRAW)
-            go = mbar_wait(&sh->raw_empty[slot], (i / C::NRAW - 1) & 1, abort_flag, p.status);
-          go = __shfl_sync(0xffffffffu, go, 0);
-#ifdef EXATTN_TEST_WITHHOLD
-          // Test build only: stop before ring index EXATTN_TEST_WITHHOLD, so that
-          // the consumers' waits run out.
-          if (i == EXATTN_TEST_WITHHOLD) go = false;
-#endif
-          if (!go) break;
-          bool v;
-          int j, scale_slot;
-          entry<kTwin>(i, jlo, total, v, j, scale_slot);
-          // (A scale slot comes round after eight tiles; the rings hold at most six
-          // between here and the softmax.)
-          if (!v && e == k) {
-            sh->k_scale[scale_slot][u] = scale.x;
-            sh->v_scale[scale_slot][u] = scale.y;
-          }
-          __syncwarp();
-          if (lane == 0)
-            mbar_arrive_expect_tx(&sh->raw_full[slot], __popc((live >> (8 * k)) & 0xffu) * (kPage * D));
-          __syncwarp();
-          if (e == k && pid >= 0)
-            bulk_load(smem + C::RAW_OFF + slot * C::RAW_BYTES + u * (kPage * D),
-                      (v ? p.v_pages : p.k_pages) + (static_cast<size_t>(pid) * p.Hkv + hkv) * (kPage * D),
-                      kPage * D, &sh->raw_full[slot]);
-          issued = i + 1;
-        }
-        pid = pid1;
-        scale = scale1;
-        pid1 = pid2;
-      }
-      // No copy may still be writing shared memory when the CTA exits.
-      if (lane == 0)
-        for (int i = max(0, issued - C::NRAW); i < issued; ++i)
-          mbar_wait_drain(&sh->raw_full[i % C::NRAW], (i / C::NRAW) & 1, p.status);
     }
   } else if (warp < 8) {
     // =============================================================== widening
-    regs_dec<kRegsWiden>();
+    regs_dec<Regs<kTwin>::kWiden>();
     const int w = warp - 4;
     constexpr int LPR = D / 16;         // lanes per row
     constexpr int RPP = 32 / LPR;       // rows per 512-byte pass
@@ -729,21 +665,94 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         }
       }
     };
-    // Raw entry i is in its slot, and the ring's slot for it is free.
-    auto ready = [&](int i) {
-      if (!mbar_wait(&sh->raw_full[i % C::NRAW], (i / C::NRAW) & 1, abort_flag, p.status)) return false;
-      return i < C::NST || mbar_wait(&sh->empty[i % C::NST], (i / C::NST - 1) & 1, abort_flag, p.status);
+    // This warp's two pages of a tile: lane 2e + u holds the number of page u of
+    // entry e of a round of 16, and its scales (with K: the softmax applies both).
+    // Numbers are read two rounds ahead and scales one, so that neither's latency
+    // is waited for.
+    const int *table = p.block_table + static_cast<size_t>(seq) * p.max_blocks;
+    const float v_unit = __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23);
+    auto page_of = [&](int i0) {
+      const int i = i0 + (lane >> 1);
+      if (i >= total) return -1;
+      bool v;
+      int j, slot;
+      entry<kTwin>(i, jlo, total, v, j, slot);
+      const int pg = j * kPagesPerTile + 2 * w + (lane & 1);
+      return pg * kPage < ck.n ? table[pg] : -1;
+    };
+    auto scales_of = [&](int i0, int pid) {
+      bool v;
+      int j, slot;
+      float2 x = make_float2(0.f, 0.f);
+      if (pid < 0) return x;
+      entry<kTwin>(i0 + (lane >> 1), jlo, total, v, j, slot);
+      if (v) return x;
+      const size_t slice = static_cast<size_t>(pid) * p.Hkv + hkv;
+      x.x = p.k_scales[slice];
+      x.y = p.v_scales[slice] * v_unit;
+      return x;
+    };
+    int pid = page_of(0), pid1 = page_of(16);  // of entry i's round, and the next
+    float2 scale = scales_of(0, pid), scale1 = make_float2(0.f, 0.f);
+    int pid2 = -1;
+    // Copies this lane's bytes of entry i of the round that `pids` is of into its
+    // raw slot: only this lane reads them, so its own wait is all they need.
+    // Slots of pages behind the keys get zeros.  (Bulk copies of the 2 KB slices,
+    // by two warps of their own, went at 12.6 bytes a cycle and SM, and bounded
+    // calls of few rows: 73 us against 70 for 20 rows over 8 K to 32 K keys.)
+    auto copy = [&](int i, int pids) {
+      if (i < total) {
+        bool v;
+        int j, slot;
+        entry<kTwin>(i, jlo, total, v, j, slot);
+        const uint8_t *pool = v ? p.v_pages : p.k_pages;
+        const uint32_t dst = smem_u32(smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int pg = __shfl_sync(0xffffffffu, pids, 2 * (i & 15) + g);
+          const uint8_t *src = pool + (static_cast<size_t>(max(pg, 0)) * p.Hkv + hkv) * (kPage * D) +
+                               row * D + piece * 16;
+#pragma unroll
+          for (int u = 0; u < PASSES; ++u)
+            copy_async16(dst + (g * PASSES + u) * 512, src + u * 512, pg < 0 ? 0 : 16);
+        }
+      }
+      copy_async_commit();
     };
     auto done = [&](int i) {
       fence_async_shared();
       mbar_arrive(&sh->full[i % C::NST]);
-      mbar_arrive(&sh->raw_empty[i % C::NRAW]);
     };
+    for (int i = 0; i < C::NRAW - 1; ++i) copy(i, pid);
     for (int i = 0; i < total; ++i) {
+      if ((i & 15) == 0) {
+        if (i > 0) {
+          pid = pid1;
+          pid1 = pid2;
+          scale = scale1;
+        }
+        scale1 = scales_of(i + 16, pid1);
+        pid2 = page_of(i + 32);
+      }
+      copy(i + C::NRAW - 1, ((i + C::NRAW - 1) >> 4) == (i >> 4) ? pid : pid1);
       bool v;
       int j, scale_slot;
       entry<kTwin>(i, jlo, total, v, j, scale_slot);
-      if (!ready(i)) break;
+#ifdef EXATTN_TEST_WITHHOLD
+      // Test build only: stop before ring index EXATTN_TEST_WITHHOLD, so that the
+      // consumers' waits run out.
+      if (i == EXATTN_TEST_WITHHOLD) break;
+#endif
+      // The ring's slot is free, and (of this lane) entry i has come.
+      const bool ok = i < C::NST || mbar_wait(&sh->empty[i % C::NST], (i / C::NST - 1) & 1, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      copy_async_wait<C::NRAW - 1>();
+      // (A scale slot comes round after eight tiles; the ring holds at most four
+      // between here and the softmax.)
+      if (!v && (lane >> 1) == (i & 15)) {
+        sh->k_scale[scale_slot][2 * w + (lane & 1)] = scale.x;
+        sh->v_scale[scale_slot][2 * w + (lane & 1)] = scale.y;
+      }
       uint8_t *dst = sRing + (i % C::NST) * C::TILE_BYTES;
       widen(smem + C::RAW_OFF + (i % C::NRAW) * C::RAW_BYTES + from, dst);
       // V tiles that some row sees only in part: their slot in v_bad, or -1.  (An
@@ -776,15 +785,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       }
       done(i);
     }
+    copy_async_wait<0>();  // no copy may still be on its way when the CTA exits
   } else {
     // ====================================================== softmax / epilogue
-    regs_inc<kRegsSoft>();
+    regs_inc<Regs<kTwin>::kSoft>();
     const int t = (warp - 8) >> 2;   // row tile of this warpgroup
     const int quarter = warp & 3;    // TMEM lane quarter this warp may access
     const int r = quarter * 32 + lane;
-    const int tl = r / p.heads;      // token of the tile; rows behind tokens * heads are idle
+    const int rr = few ? lane : r;   // row of this thread
+    const int tl = rr / p.heads;     // token of the tile; rows behind tokens * heads are idle
     const int tok = tok0 + (kTwin ? 0 : t * p.tokens) + tl;
-    const int hq = h0 + r - tl * p.heads;
+    const int hq = h0 + rr - tl * p.heads;
     const bool valid = tl < p.tokens && tok < ck.nq;
     const int jst = t == 0 ? js0 : js1, jen = t == 0 ? je0 : je1;
     const int nt = jen - jst;
@@ -832,7 +843,79 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     float l = 0.f;
     bool poison = false;  // the row sees a value that is no number and was left out
     bool ok = true;
-    for (int jj = 0; jj < nt; ++jj) {
+    if (few) {
+      // The softmax of this thread's row over columns 32 * quarter .. of every
+      // tile, with a reference and a sum of its own; P is zero in the others.
+      // Else as below.
+      const int c0 = 32 * quarter;
+      for (int jj = 0; jj < nt; ++jj) {
+        const int j = jst + jj;
+        const int hi = min(min(BN, ck.n - j * BN), ck.ctx + tok - j * BN + 1) - c0;
+        const int lo = (p.window > 0 ? ck.ctx + min(tok, ck.nq - 1) - p.window + 1 - j * BN : 0) - c0;
+        const bool masked = !__all_sync(0xffffffffu, lo <= 0 && hi >= 32);
+        ok = mbar_wait(&sh->s_full[t], jj & 1, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[32], pk[16];
+        tmem_ld32(s_addr + c0, sv);
+        const int slot = (2 * jj + t) % kScaleRing;
+        const float2 ks = *reinterpret_cast<const float2 *>(&sh->k_scale[slot][2 * quarter]);
+        const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[slot][2 * quarter]);
+        const float cp[2] = {ks.x * c_row, ks.y * c_row};
+        float vp[2] = {vs.x, vs.y};
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          if (!(fabsf(vp[g]) <= 3.4028235e38f)) {
+            poison |= lo < kPage * (g + 1) && hi > kPage * g;
+            vp[g] = 0.f;
+          }
+        tmem_ld_wait(sv);
+        const float rb = kAlibi ? slope2 * static_cast<float>(j * BN + c0 - (ck.ctx + tok)) : 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+#pragma unroll
+          for (int k = i; k < i + 2; ++k) {
+            float x = __uint_as_float(sv[k]) * cp[k / kPage];
+            if (kAlibi) x += fmaf(slope2, static_cast<float>(k), rb);
+            if (masked && (k < lo || k >= hi)) x = -INFINITY;
+            sv[k] = __float_as_uint(x);
+          }
+          m0 = fmaxf(m0, __uint_as_float(sv[i]));
+          m1 = fmaxf(m1, __uint_as_float(sv[i + 1]));
+        }
+        const float m_new = fmaxf(m, fmaxf(m0, m1));
+        const bool resc = m_new > m + 8.0f;
+        const float alpha = resc ? ex2(m - m_new) : 1.0f;
+        if (resc) m = m_new;
+        l *= alpha;
+        if (jj > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t ov[32];
+            tmem_ld32(o_addr + cc * 32, ov);
+            tmem_ld_wait(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(o_addr + cc * 32, ov);
+          }
+        }
+        const float ones[2] = {1.f, 1.f};
+        l += exp_cols(sv, ones, vp, m == -INFINITY ? 0.f : m, pk);
+        const uint32_t zero[16] = {};
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g == quarter) tmem_st16(s_addr + 16 * g, pk);
+          else tmem_st16(s_addr + 16 * g, zero);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sh->p_half[t]);
+        mbar_arrive(&sh->p_full[t]);
+      }
+    }
+    for (int jj = few ? nt : 0; jj < nt; ++jj) {
       const int j = jst + jj;
       // Visible columns [lo, hi) of this row.  (A row without a token takes one
       // that forces no masking on a warp whose real rows need none.)
@@ -888,7 +971,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         // max-first step below would have kept the reference too.
         tmem_ld64(s_addr, sv);
         tmem_ld_wait64(sv);
-        const float l0 = exp_half(sv, cp, vp, m, pk);
+        const float l0 = exp_cols(sv, cp, vp, m, pk);
         if (__all_sync(0xffffffffu, l0 <= 255.0f)) {
           first_done = true;
           tmem_ld64(s_addr + 64, sv);
@@ -898,7 +981,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           mbar_arrive(&sh->p_half[t]);
           l += l0;
           tmem_ld_wait64(sv);
-          const float l1 = exp_half(sv, cp + 4, vp + 4, m, pk);
+          const float l1 = exp_cols(sv, cp + 4, vp + 4, m, pk);
           if (__all_sync(0xffffffffu, l1 <= 255.0f)) {
             l += l1;
             store_half(s_addr + 32, pk);
@@ -976,7 +1059,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       for (int h = first_done; h < 2; ++h) {
         scaled_half(h);
         const float vh[4] = {h ? vp[4] : vp[0], h ? vp[5] : vp[1], h ? vp[6] : vp[2], h ? vp[7] : vp[3]};
-        l += exp_half(sv, ones, vh, m_use, pk);
+        l += exp_cols(sv, ones, vh, m_use, pk);
         store_half(s_addr + 32 * h, pk);
         tmem_st_wait();
         tc_fence_before();
@@ -998,9 +1081,72 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         for (int i = lo; i < hi; ++i) poison |= (sh->v_bad[e][i >> 5] >> (i & 31) & 1u) != 0;
       }
     }
+    if (few) {
+      // Eight partial results of every row, over disjoint keys: joined through
+      // the ring, which is free once both tiles' products are done.
+      soft_barrier();
+      float4 *all = reinterpret_cast<float4 *>(sRing);
+      const int me = warp - 8;
+      all[me * 32 + lane] = make_float4(m, l, poison ? 1.f : 0.f, 0.f);
+      soft_barrier();
+      float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = all[i * 32 + lane];
+        mm = fmaxf(mm, x.x);
+        poison |= x.z != 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = all[i * 32 + lane];
+        if (x.y != 0.f) sum += x.y * ex2(x.x - mm);
+      }
+      const bool use = ok && nt > 0 && l != 0.f;
+      const float weight = use ? ex2(m - mm) * (poison ? NAN : scalbnf(1.0f / sum, v_exp)) : 0.f;
+      constexpr int kRow = D + 4;  // floats; keeps a store's eight lanes in different banks
+      float *joint = reinterpret_cast<float *>(sRing + 8 * 32 * sizeof(float4));
+      tc_fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t ov[32];
+        tmem_ld32(o_addr + cc * 32, ov);
+        tmem_ld_wait(ov);
+        float4 *dst = reinterpret_cast<float4 *>(joint + (me * 32 + lane) * kRow + cc * 32);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = use ? __uint_as_float(ov[i + k]) * weight : 0.f;
+          dst[i >> 2] = make_float4(x[0], x[1], x[2], x[3]);
+        }
+      }
+      soft_barrier();
+      for (int i = static_cast<int>(threadIdx.x) - 256; i < rows_here * (D / 4); i += 256) {
+        const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 y = *reinterpret_cast<const float4 *>(joint + (k * 32 + row) * kRow + c);
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        if (!p.split) {
+          const int tk = row / p.heads;
+          const size_t at = static_cast<size_t>(ck.q0 + tok0 + tk) * p.Hq + h0 + row - tk * p.heads;
+          *reinterpret_cast<uint2 *>(p.o + at * D + c) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+        } else {
+          *reinterpret_cast<float4 *>(p.o_part + (static_cast<size_t>(lin) * p.rows_cap + row) * D + c) = x;
+        }
+      }
+      if (me == 0 && valid) {
+        const float l2 = sum != 0.f ? mm + log2f(sum) : -INFINITY;
+        if (!p.split) p.lse[out_row] = l2 * 0.6931471805599453f;
+        else p.l2_part[static_cast<size_t>(lin) * p.rows_cap + lane] = l2;
+      }
+      ok = false;  // nothing more for these warps
+    }
     // (l != 0 for a NaN too; 0 for a row that saw no key here: part of them only.)
     float a0 = l != 0.f ? 1.f : 0.f, a1 = 0.f;  // weights of the O tiles
-    if constexpr (kTwin) {
+    if (kTwin && !few) {
       // The tiles hold partial results of the same rows over disjoint keys: tile
       // 1's threads publish their m and l, and tile 0's join them.
       float2 *xfer = reinterpret_cast<float2 *>(smem + C::XFER_OFF);
