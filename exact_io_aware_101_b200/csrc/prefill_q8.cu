@@ -23,8 +23,14 @@
 //                   128-byte-swizzled layout that the MMAs read;
 //      warps 8-11   softmax, correction and epilogue of tile 0, warps 12-15 of
 //                   tile 1; before that they bring the tiles' queries to f16.
-//    Measured on the chunked workload (16 chunks of 512, Hq = 32, Hkv = 8, d =
-//    128): see the table of operators.
+//  * What bounds it, and what it measured (B200, E4M3, d = 128, 32 query and 8 K/V
+//    heads).  16 chunks of 512 tokens after up to 7680: the chain of a row tile,
+//    product -> softmax -> product, 3600 cycles a key tile against the tensor
+//    cores' 2048; 560 us, 949 TFLOP/s or 58 % of the measured bf16 rate, and 600
+//    us in a run long enough for the power limit.  Four sequences of five tokens
+//    (20 rows a K/V head) over 8 K to 32 K keys, INT8: the widening, about 900
+//    cycles a tile, beside some 10 us of launches, plan and joining; 70 us, 2.5
+//    TB/s of codes or 39 % of the measured copy rate.
 //  * Exactness.  Codes are exact in f16.  Queries are scaled by a power of two
 //    per row before rounding to f16, exact for elements within 2^28 of the
 //    row's largest.  The K scale multiplies the f32 scores, per page.  The V
@@ -34,10 +40,15 @@
 //    scale times the row's largest P lose bits.  Scaling the codes on their way
 //    instead costs two roundings, and as much time: 600 us for the 16 chunks
 //    either way, in a run long enough for the power limit.)
-//  * Few rows and long keys: when the row tiles alone leave SMs idle, each
-//    tile's keys are split over several CTAs, which write normalised partials
-//    and their log2-sum-exps to the workspace; a second kernel, scheduled
-//    behind the first, joins them.
+//  * Few rows and long keys.  A chunk that fits one row tile gives both tiles the
+//    same rows and half of the CTA's keys each ("twin"), which overlaps what one
+//    tile alone does in turn: 146 us -> 89 us for the 20 rows above, with the
+//    even split below.  With at most 32 rows every quarter of a tile's lanes
+//    holds all of them and its warp works on a quarter of the columns.  When the
+//    row tiles alone leave SMs idle, each tile's keys are split over several
+//    CTAs, by each sequence's length, which write normalised partials and their
+//    log2-sum-exps to the workspace; a second kernel, scheduled behind the first,
+//    joins them.
 //  * NaN behind the mask: a masked score is replaced, whatever it was.  In the
 //    P V product a zero weight would not cancel a NaN value, so in tiles that
 //    some row sees only in part such values enter as zeros and are noted by
@@ -1288,8 +1299,7 @@ Cut cut(int S, int Hq, int Hkv, int max_q, int max_blocks) {
   c.tokens = BM / c.heads;
   const bool many = max_blocks > kPagesPerTile;  // more than one key tile
   // Chunks that fit one row tile: both tiles take the same rows and half the
-  // keys each, which overlaps what one tile alone does in turn (20 rows over
-  // 8 K to 32 K keys, 4 sequences: see the table of operators).
+  // keys each (both sides measured: see the top of the file).
   c.twin = many && max_q <= c.tokens;
   c.span = c.twin ? c.tokens : 2 * c.tokens;
   c.pairs = (max_q + c.span - 1) / c.span;

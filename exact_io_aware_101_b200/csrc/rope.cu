@@ -13,13 +13,17 @@
 //
 // What bounds it: HBM.  Every row is read once (in the gradient x and dy) and
 // written once, and the arithmetic of a row is about 100 operations per 16
-// elements.  So:
+// elements.  Measured (B200): norm and rotation of 4 x 4096 tokens of 40 bf16
+// heads, d = 128, 60 us (5.6 TB/s, 85 % of the measured copy rate), its gradient
+// 100 us (5.0 TB/s, bounded by the bytes that four blocks of 128 registers a
+// thread keep on their way), a partial fp32 rotation of 2 x 2047 tokens of 32
+// heads, d = 64, 10.9 us (6.2 TB/s), one decode step of 64 tokens 3.1 us.  So:
 //  * One thread holds the same 16 elements (8 pairs) of its rows and walks the
 //    heads of one token, q's and then k's: the cosines and sines of its 8 pairs
 //    stay in registers, worked out once for all those heads.  LPR = d/16 lanes
 //    hold a row, and a norm's two sums are log2(LPR) shuffles.
-//  * Each lane moves 16-byte words, and the next kAhead rows are on their way,
-//    packed as they lie in memory, while a row is worked on.  (Four rows loaded
+//  * Each lane moves 16-byte words, and the next row (or two) is on its way,
+//    packed as it lies in memory, while a row is worked on.  (Four rows loaded
 //    and unpacked together took 128 registers: 95 us for 4 x 4096 tokens of 40
 //    bf16 heads with norms, and 197 us for the gradient.)  Half layouts whose rot
 //    is not a multiple of two such words would put the partner elements at odd
@@ -52,7 +56,7 @@ constexpr int kThreads = 128;
 constexpr int kSMs = 148;
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-enum Mode { kHalf, kPairs, kScalar };   // where a thread's pairs lie (see load_row)
+enum Mode { kHalf, kPairs, kScalar };   // where a thread's pairs lie (see Slots)
 enum Op { kTurn, kNormTurn, kNormTurnBwd };
 
 // One of the two tensors of a call: q or k.

@@ -319,7 +319,8 @@ EXATTN_API attn_status_t attn_decode_paged_q8(const void *q, const void *k_pages
  *   max_q        an upper bound of every qlen_s (sizes the grid)
  * Slots and pages that hold none of the chunk's tokens stay as they are, but for
  * the earlier tokens of a chunk's first page.  A page that is written must be
- * one sequence's alone; two that write it leave either's bytes.  A sequence
+ * one sequence's alone, once; what several writers of one page leave is any mix
+ * of theirs.  A sequence
  * whose lengths are inconsistent (as for attn_prefill_paged) is skipped, and so
  * is a page id outside [0, num_pages); both set ATTN_DEV_BAD_PAGE in the word of
  * attn_device_status, and no out-of-range address is dereferenced.  T == 0 or
@@ -365,7 +366,8 @@ EXATTN_API attn_status_t attn_kv_read_paged_q8(
  *                where that is 0.  Calls that may run at the same time need one
  *                each.
  * Inside the kernel queries are rounded to f16 after a per-row power-of-two
- * normalisation, the V elements (scale * code) and P to f16; scores, sums and
+ * normalisation, and P times the V scale to f16, relative to the largest V scale
+ * of the keys at hand (terms 2^-19 of it and smaller lose bits); scores, sums and
  * outputs accumulate in float32.
  */
 EXATTN_API size_t attn_prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q, int d,

@@ -10,9 +10,9 @@ together below 2^-21.  A norm adds its sum of squares (an element passes at most
 16 + 4 additions, 20 * 2^-24, halved by the root), the root, and two products:
 below 2^-20 in all, 2^-19 with the rotation.  The gradient's dx has two such
 factors and the row's second sum (at most another 20 * 2^-24): 2^-18 of its size.
-A weight's gradient adds n terms, each off by 2^-19 of its size, in partial sums
-of at most 16 heads by the tiles of a block, here at most 64 additions in a row,
-and 6 + 40 more across the block and the blocks: 2^-17 of the sum of sizes.
+A weight's gradient adds n terms, each off by 2^-19 of its size: an element passes
+at most 48 additions over heads here, 3 over a block's tiles, 6 across the block
+and 24 across the blocks, 81 * 2^-24: together below 2^-17 of the sum of sizes.
 """
 from __future__ import annotations
 
