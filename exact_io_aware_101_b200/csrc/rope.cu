@@ -462,9 +462,10 @@ Cut cut(long long tokens, int heads, int d, int op, int size) {
   // kAngles heads; all blocks take as many turns as they fill the slots.
   // More groups balance the turns better and work the angles out more often.
   constexpr int kAngles = 3;
-  Cut c{heads, 1, 0};
+  Cut c{1, heads, 0};
   long long best = -1, turns = 1;
-  for (int g = 1; g <= heads && g <= 256; ++g) {
+  // (A head a block where all of those run at once.)
+  for (int g = 1; tiles * heads > slots && g <= heads && g <= 64; ++g) {
     const int per = (heads + g - 1) / g;
     const long long t = (tiles * g + slots - 1) / slots, cost = t * (per + kAngles);
     if (best < 0 || cost < best) {
