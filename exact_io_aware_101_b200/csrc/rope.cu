@@ -14,16 +14,15 @@
 // What bounds it: HBM.  Every row is read once (in the gradient x and dy) and
 // written once, and the arithmetic of a row is about 100 operations per 16
 // elements.  Measured (B200): norm and rotation of 4 x 4096 tokens of 40 bf16
-// heads, d = 128, 60 us (5.6 TB/s, 85 % of the measured copy rate), its gradient
-// 100 us (5.0 TB/s, bounded by the bytes that four blocks of 128 registers a
-// thread keep on their way), a partial fp32 rotation of 2 x 2047 tokens of 32
-// heads, d = 64, 10.9 us (6.2 TB/s), one decode step of 64 tokens 3.1 us.  So:
+// heads, d = 128, 56 us (6.0 TB/s, 92 % of the measured copy rate), its gradient
+// 89 us (5.7 TB/s, 87 %), a partial fp32 rotation of 2 x 2047 tokens of 32
+// heads, d = 64, 11.0 us (6.2 TB/s), one decode step of 64 tokens 3.3 us.  So:
 //  * One thread holds the same 16 elements (8 pairs) of its rows and walks the
 //    heads of one token, q's and then k's: the cosines and sines of its 8 pairs
 //    stay in registers, worked out once for all those heads.  LPR = d/16 lanes
 //    hold a row, and a norm's two sums are log2(LPR) shuffles.
-//  * Each lane moves 16-byte words, and the next row (or two) is on its way,
-//    packed as it lies in memory, while a row is worked on.  (Four rows loaded
+//  * Each lane moves 16-byte words, and the next rows (one to three) are on their
+//    way, packed as they lie in memory, while a row is worked on.  (Four rows loaded
 //    and unpacked together took 128 registers: 95 us for 4 x 4096 tokens of 40
 //    bf16 heads with norms, and 197 us for the gradient.)  Half layouts whose rot
 //    is not a multiple of two such words would put the partner elements at odd
@@ -228,6 +227,17 @@ struct Slots {
   }
 };
 
+// 16 bytes from global to shared memory behind this thread's back; a group of
+// them is closed, and waited for but for the N newest.
+__device__ __forceinline__ void copy_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Sum over the LPR lanes of a row.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -236,13 +246,20 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Blocks that an SM holds at a time (the registers' limit is set to that), and
-// rows on their way while one is worked on: more of either spills.
+// Blocks that an SM holds at a time (the registers' limit is set to that; one more
+// spills), and rows on their way while one is worked on.  The norms' rows wait in
+// shared memory, where words lie as they do in global memory; a bare turn, which
+// has registers to spare, and layouts of single elements hold theirs in registers.
+// (In registers: 60 us for the norm and 100 for its gradient instead of 56 and 89,
+// 4 x 4096 tokens of 40 bf16 heads.  Staged: 11.4 us for the fp32 turn of 2 x 2047
+// tokens instead of 11.0.)
 constexpr int blocks_per_sm(int op, int size) {
-  return op == kTurn ? 7 : (op == kNormTurn ? 5 : (size == 4 ? 3 : 4));
+  return op == kTurn ? 7 : (op == kNormTurn ? (size == 4 ? 5 : 6) : (size == 4 ? 3 : 4));
 }
+constexpr bool rows_staged(int mode, int op) { return op != kTurn && mode != kScalar; }
 constexpr int rows_ahead(int mode, int op, int size) {
-  return op == kNormTurnBwd || mode == kScalar || size == 4 ? 1 : 2;
+  return rows_staged(mode, op) ? (op == kNormTurn ? (size == 4 ? 2 : 3) : (size == 4 ? 1 : 2))
+                               : (op == kTurn && mode != kScalar && size == 2 ? 2 : 1);
 }
 
 // Block (x, y): group y of the heads, token tiles x, x + gridDim.x, ...
@@ -251,11 +268,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(OP, sizeof(T))) rope_k
   constexpr int LPR = D / 16, TT = kThreads / LPR;
   constexpr int A = rows_ahead(MODE, OP, sizeof(T));
   constexpr bool kBwd = OP == kNormTurnBwd;
+  constexpr bool kStaged = rows_staged(MODE, OP);
   if constexpr (kBwd) grid_dependents_launch();
   using S = Slots<T, D, MODE>;
   const int lane = threadIdx.x % LPR, slot_row = threadIdx.x / LPR;
   const S sl(lane, p.rot);
   const int hb = blockIdx.y * p.per_group, he = hb + p.per_group;
+  // Rows on their way: this thread's words of A rows, and of the one at hand.
+  constexpr int kTensors = kBwd ? 2 : 1;
+  __shared__ uint4 stage[kStaged ? A + 1 : 1][kStaged ? kTensors * S::W : 1][kThreads];
   // Gradient: this thread's sums of its 16 elements' dw, for q and for k.
   __shared__ float sums[kBwd ? 2 : 1][kBwd ? 16 : 1][kThreads];
   if constexpr (kBwd) {
@@ -320,63 +341,99 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(OP, sizeof(T))) rope_k
       const T *x = static_cast<const T *>(sd.x) + bi * sd.xb + n * sd.xn;
       T *y = static_cast<T *>(sd.y) + bi * sd.yb + n * sd.yn;
       const T *dy = kBwd ? static_cast<const T *>(sd.dy) + bi * sd.gb + n * sd.gn : nullptr;
-      typename S::Held xr[A], gr[kBwd ? A : 1];
+      // Row h's words to their stage, closed as a group (an empty one past the last).
+      auto ahead = [&](int h) {
+        if constexpr (kStaged) {
+          if (h < h1) {
+            uint4(*at)[kThreads] = stage[(h - h0) % (A + 1)];
 #pragma unroll
-      for (int i = 0; i < A; ++i)
-        if (h0 + i < h1) {
-          sl.load(x + (h0 + i) * sd.xh, xr[i]);
-          if constexpr (kBwd) sl.load(dy + (h0 + i) * sd.gh, gr[i]);
-        }
-      for (int hh = h0; hh < h1; hh += A) {
-#pragma unroll
-        for (int i = 0; i < A; ++i) {
-          const int h = hh + i;
-          if (h >= h1) break;  // (the same for every lane)
-          float a[8], b[8], c[kBwd ? 8 : 1], e[kBwd ? 8 : 1];
-          sl.get(xr[i], a, b);
-          if constexpr (kBwd) sl.get(gr[i], c, e);
-          // (In place, a row's lanes store after all of them have loaded it; the
-          // rows on their way are other rows.)
-          if (h + A < h1) {
-            sl.load(x + (h + A) * sd.xh, xr[i]);
-            if constexpr (kBwd) sl.load(dy + (h + A) * sd.gh, gr[i]);
-          }
-          if constexpr (OP == kTurn) {
-            turn(a, b);
-          } else {
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss += a[j] * a[j] + b[j] * b[j];
-            const float r = __frsqrt_rn(row_sum<LPR>(ss) * (1.f / D) + p.eps);
-            if constexpr (OP == kNormTurn) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                a[j] = a[j] * r * wa[j];
-                b[j] = b[j] * r * wb[j];
-              }
-              turn(a, b);
-            } else {
-              float dot = 0.f;
-              turn(c, e);  // u: sign is -1 here
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                a[j] *= r;  // xhat
-                b[j] *= r;
-                ga[j] += c[j] * a[j];
-                gb[j] += e[j] * b[j];
-                c[j] *= wa[j];
-                e[j] *= wb[j];
-                dot += c[j] * a[j] + e[j] * b[j];
-              }
-              dot = row_sum<LPR>(dot) * (1.f / D);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                a[j] = r * (c[j] - a[j] * dot);
-                b[j] = r * (e[j] - b[j] * dot);
-              }
+            for (int w = 0; w < S::W; ++w) {
+              copy_async16(&at[w][threadIdx.x], x + h * sd.xh + sl.at[w]);
+              if constexpr (kBwd) copy_async16(&at[S::W + w][threadIdx.x], dy + h * sd.gh + sl.at[w]);
             }
           }
-          if (live) sl.store(y + h * sd.yh, a, b);
+          copy_async_commit();
+        }
+      };
+      // One row, loaded as r0 (and its gradient g0).  In place, its lanes store after
+      // all of them have read it; the rows on their way are other rows.
+      auto work = [&](int h, const typename S::Held &r0, const typename S::Held &g0) {
+        float a[8], b[8], c[kBwd ? 8 : 1], e[kBwd ? 8 : 1];
+        sl.get(r0, a, b);
+        if constexpr (kBwd) sl.get(g0, c, e);
+        if constexpr (OP == kTurn) {
+          turn(a, b);
+        } else {
+          float ss = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss += a[j] * a[j] + b[j] * b[j];
+          const float r = __frsqrt_rn(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+          if constexpr (OP == kNormTurn) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              a[j] = a[j] * r * wa[j];
+              b[j] = b[j] * r * wb[j];
+            }
+            turn(a, b);
+          } else {
+            float dot = 0.f;
+            turn(c, e);  // u: sign is -1 here
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              a[j] *= r;  // xhat
+              b[j] *= r;
+              ga[j] += c[j] * a[j];
+              gb[j] += e[j] * b[j];
+              c[j] *= wa[j];
+              e[j] *= wb[j];
+              dot += c[j] * a[j] + e[j] * b[j];
+            }
+            dot = row_sum<LPR>(dot) * (1.f / D);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              a[j] = r * (c[j] - a[j] * dot);
+              b[j] = r * (e[j] - b[j] * dot);
+            }
+          }
+        }
+        if (live) sl.store(y + h * sd.yh, a, b);
+      };
+      if constexpr (kStaged) {
+#pragma unroll
+        for (int i = 0; i < A; ++i) ahead(h0 + i);
+        for (int h = h0; h < h1; ++h) {
+          // (The stage that row h + A goes to held row h - 1, which has been used.)
+          ahead(h + A);
+          copy_async_wait<A>();
+          const uint4(*at)[kThreads] = stage[(h - h0) % (A + 1)];
+          typename S::Held r0, g0;
+#pragma unroll
+          for (int w = 0; w < S::W; ++w) {
+            r0.w[w] = at[w][threadIdx.x];
+            if constexpr (kBwd) g0.w[w] = at[S::W + w][threadIdx.x];
+          }
+          work(h, r0, g0);
+        }
+      } else {
+        typename S::Held xr[A], gr[A];
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+          if (h0 + i < h1) {
+            sl.load(x + (h0 + i) * sd.xh, xr[i]);
+            if constexpr (kBwd) sl.load(dy + (h0 + i) * sd.gh, gr[i]);
+          }
+        for (int hh = h0; hh < h1; hh += A) {
+#pragma unroll
+          for (int i = 0; i < A; ++i) {
+            const int h = hh + i;
+            if (h >= h1) break;  // (the same for every lane)
+            const typename S::Held r0 = xr[i], g0 = gr[i];
+            if (h + A < h1) {
+              sl.load(x + (h + A) * sd.xh, xr[i]);
+              if constexpr (kBwd) sl.load(dy + (h + A) * sd.gh, gr[i]);
+            }
+            work(h, r0, g0);
+          }
         }
       }
       if constexpr (kBwd) {
@@ -394,7 +451,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(OP, sizeof(T))) rope_k
   if constexpr (kBwd) {
     // The block's row of sums: lanes of a warp that hold the same elements
     // first, then the warps, in a fixed order.
-    __shared__ float by_warp[kThreads / 32][D];
+    static_assert(!kStaged || sizeof(stage) >= kThreads / 32 * D * sizeof(float), "by_warp lies over the stages");
+    __shared__ float own[kStaged ? 1 : kThreads / 32][kStaged ? 1 : D];
+    float(*by_warp)[D] = kStaged ? reinterpret_cast<float(*)[D]>(&stage[0][0][0]) : reinterpret_cast<float(*)[D]>(&own[0][0]);
+    __syncthreads();  // every thread is through with its stages
     const int warp = threadIdx.x >> 5;
     const long long block = static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x;
     const long long blocks = static_cast<long long>(gridDim.y) * gridDim.x;
