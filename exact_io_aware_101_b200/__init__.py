@@ -866,6 +866,8 @@ def _rope_args(q, k, positions, inv_freq, like_q, like_k):
         if ks != ((N, Hkv, d) if nd == 3 else (B, Hkv, N, d)):
             raise ValueError("k must be %s matching q %s"
                              % ("[T, Hkv, d]" if nd == 3 else "[B, Hkv, N, d]", tuple(qs)))
+        if Hkv == 0:
+            raise ValueError("k has no heads; None stands for no keys")
     elif any(t is not None for _, t in like_k):
         raise ValueError("%s given without k" % like_k[0][0])
     if not isinstance(positions, torch.Tensor) or not isinstance(inv_freq, torch.Tensor):

@@ -413,7 +413,9 @@ EXATTN_API attn_status_t attn_rope(
  * each head (no counterpart on the pages):
  *   z = q_weight * x * (mean(x^2) + eps)^(-1/2),  then the rotation of z,
  * with k_weight for the keys.  Weights: [d] of dtype, shared by the heads; eps
- * finite and > 0.  Other arguments as for attn_rope.
+ * finite and > 0.  Squares are summed in float32: a row of elements whose sum of
+ * squares passes its range (one of 2^64) is divided by infinity.  Other arguments
+ * as for attn_rope.
  */
 EXATTN_API attn_status_t attn_norm_rope(
     const void *q, const attn_strides_t *q_strides, const void *q_weight, void *q_out,

@@ -233,6 +233,17 @@ def test_binding_rotations_check_shapes_first():
         ea.attn_norm_rope_bwd(q, k, w, w, q, q, pos, f)
 
 
+def test_binding_refuses_keys_without_heads():
+    """(Their weights' gradient would be left as it was allocated.)"""
+    q, k, pos, f = torch.zeros(2, 4, 8, 64), torch.zeros(2, 0, 8, 64), torch.zeros(8, dtype=torch.int32), \
+        torch.zeros(32, dtype=torch.float64)
+    w = torch.zeros(64)
+    for call in (lambda: ea.attn_rope(q, k, pos, f), lambda: ea.attn_norm_rope(q, k, w, w, pos, f),
+                 lambda: ea.attn_norm_rope_bwd(q, k, w, w, q, k, pos, f)):
+        with pytest.raises(ValueError, match="no heads"):
+            call()
+
+
 def test_binding_cache_calls_check_shapes_first():
     P, Hkv, d, S = 6, 2, 64, 3
     kp = torch.zeros(P, Hkv, 16, d, dtype=torch.int8)
