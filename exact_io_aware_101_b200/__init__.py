@@ -681,8 +681,8 @@ def attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_tab
     vh, vt = _row_strides(v)
     _kv_write(index, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, k_pages.data_ptr(),
               v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), KV_FORMATS[kv_format],
-              block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S, Hkv, T, int(max_q),
-              d, page_size, max_blocks, num_pages, _stream(k))
+              block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S, Hkv, T,
+              min(int(max_q), T), d, page_size, max_blocks, num_pages, _stream(k))
 
 
 def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
@@ -720,7 +720,7 @@ def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq
     _kv_read(index, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
              v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
              seq_lens.data_ptr(), cu_q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dtype], S,
-             Hkv, T, int(max_q), d, page_size, max_blocks, num_pages, _stream(k))
+             Hkv, T, min(int(max_q), T), d, page_size, max_blocks, num_pages, _stream(k))
     return k, v
 
 
@@ -763,7 +763,8 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     if alibi_slopes is not None:
         _check(alibi_slopes, "alibi_slopes", torch.float32, 1)
         slopes_ptr = alibi_slopes.data_ptr()
-    need = prefill_q8_workspace_bytes(S, Hq, Hkv, T, int(max_q), d, max_blocks, page_size)
+    max_q = min(int(max_q), T)  # (no chunk is longer)
+    need = prefill_q8_workspace_bytes(S, Hq, Hkv, T, max_q, d, max_blocks, page_size)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     if workspace is not None:
@@ -772,7 +773,8 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     _prefill_q8(index, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
                 v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
                 seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Hq, Hkv,
-                T, int(max_q), d, page_size, max_blocks, num_pages, float(scale), int(window),
+                T, max_q, d, page_size, max_blocks, num_pages, float(scale),
+                min(int(window), 2**31 - 1),
                 slopes_ptr, workspace.data_ptr() if workspace is not None else None,
                 workspace.numel() if workspace is not None else 0, _stream(q))
     return out, lse

@@ -6,6 +6,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -329,6 +330,7 @@ attn_status_t attn_kv_write_paged_q8(
   for (long long v_ : strides)
     if (v_ < 0 || v_ % 8 != 0 || v_ > (1LL << 44)) return ATTN_ERR_INVALID_ARG;
   if (T == 0 || max_q == 0) return ATTN_OK;
+  max_q = std::min(max_q, T);  // (no chunk is longer)
   if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID_ARG;
   unsigned *status = nullptr;
   bool sm100 = false;
@@ -350,6 +352,7 @@ attn_status_t attn_kv_read_paged_q8(
   if (st != ATTN_OK) return st;
   if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
   if (T == 0 || max_q == 0) return ATTN_OK;
+  max_q = std::min(max_q, T);  // (no chunk is longer)
   if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID_ARG;
   unsigned *status = nullptr;
   bool sm100 = false;
@@ -365,7 +368,7 @@ size_t attn_prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q,
   if (S <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || T <= 0 || max_q <= 0 || max_blocks <= 0 ||
       page_size != 16 || (d != 64 && d != 128))
     return 0;
-  return prefill_q8_workspace_bytes(S, Hq, Hkv, T, max_q, d, max_blocks);
+  return prefill_q8_workspace_bytes(S, Hq, Hkv, T, std::min(max_q, T), d, max_blocks);
 }
 
 attn_status_t attn_prefill_paged_q8(
@@ -382,6 +385,7 @@ attn_status_t attn_prefill_paged_q8(
       (alibi_slopes && !aligned4(alibi_slopes)) || static_cast<long long>(T) * Hq >= (1LL << 31))
     return ATTN_ERR_INVALID_ARG;
   if (T == 0 || max_q == 0) return ATTN_OK;
+  max_q = std::min(max_q, T);  // (no chunk is longer)
   if (!aligned16(q) || !aligned16(o) || !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
   const size_t need = prefill_q8_workspace_bytes(S, Hq, Hkv, T, max_q, d, max_blocks);
   if (need > 0 && (!aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;

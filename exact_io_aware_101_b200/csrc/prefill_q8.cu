@@ -1302,7 +1302,7 @@ Cut cut(int S, int Hq, int Hkv, int max_q, int max_blocks) {
   // keys each (both sides measured: see the top of the file).
   c.twin = many && max_q <= c.tokens;
   c.span = c.twin ? c.tokens : 2 * c.tokens;
-  c.pairs = (max_q + c.span - 1) / c.span;
+  c.pairs = (max_q - 1) / c.span + 1;
   c.rows_cap = (max_q < c.span ? max_q : c.span) * c.heads;
   c.ctas = static_cast<long long>(S) * Hkv * n * c.pairs;
   // Fewer work items than SMs: their keys are split over as many CTAs.
@@ -1405,7 +1405,7 @@ attn_status_t launch_prefill_paged_q8(const void *q, const void *k_pages, const 
   p.split = c.split;
   p.rows_cap = c.rows_cap;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.window = window;
+  p.window = window < max_blocks * kPage ? window : 0;  // (one past every length hides nothing)
   const bool e4m3 = kv_format == ATTN_KV_E4M3;
   if (d == 128)
     return e4m3 ? launch_variant<128, ATTN_KV_E4M3>(p, c, stream) : launch_variant<128, ATTN_KV_INT8>(p, c, stream);

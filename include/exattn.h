@@ -316,7 +316,8 @@ EXATTN_API attn_status_t attn_decode_paged_q8(const void *q, const void *k_pages
  *   k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, kv_format
  *                as for attn_decode_paged_q8, the pages and scales (in, out)
  *   cu_q         [S+1] int32, non-decreasing, cu_q[0] = 0, cu_q[S] <= T
- *   max_q        an upper bound of every qlen_s (sizes the grid)
+ *   max_q        an upper bound of every qlen_s (sizes the grid; what passes T is
+ *                taken as T)
  * Slots and pages that hold none of the chunk's tokens stay as they are, but for
  * the earlier tokens of a chunk's first page.  A page that is written must be
  * one sequence's alone, once; what several writers of one page leave is any mix

@@ -184,6 +184,14 @@ def test_prefill_workspace(lib):
         assert f(**dict(dict(S=4, Hq=8, Hkv=4, T=20, max_q=5, d=128, max_blocks=2048), **bad)) == 0
 
 
+def test_prefill_workspace_of_a_loose_bound():
+    """No chunk is longer than T: a bound past it asks for what T does."""
+    f = ea.prefill_q8_workspace_bytes
+    for S, T in ((1, 5), (3, 700), (100, 4000)):
+        for most in (T + 1, 1 << 20, 2**31 - 256, 2**31 - 1):
+            assert f(S, 8, 8, T, most, 128, 4096) == f(S, 8, 8, T, T, 128, 4096)
+
+
 def test_dtype_codes_match_the_header():
     import os
     import re

@@ -129,6 +129,23 @@ def test_every_cut(qlens, ctxs, Hq, Hkv, d, split, fmt):
     assert ea.device_status() == 0
 
 
+@pytest.mark.parametrize("qlens,ctxs,d", [([1, 5], [700, 0], 128), ([200, 3], [0, 400], 64)])
+def test_loose_bounds(qlens, ctxs, d):
+    """A chunk bound past T is T, and a window past every length is none."""
+    st = make(qlens, ctxs, 4, 2, d, "int8", seed=d)
+    dv = on_gpu(st)
+    want = run(dv, "int8", max_q=sum(qlens))
+    check(*want, reference(st, "int8"))
+    for kw in (dict(max_q=2**31 - 1), dict(max_q=2**32 + 1), dict(max_q=sum(qlens), window=2**31 - 1),
+               dict(max_q=2**31 - 1, window=2**32 + 3)):
+        for got, w in zip(run(dv, "int8", **kw), want):
+            assert torch.equal(got, w), kw
+    k = [ea.attn_kv_read_paged_q8(*(dv[n] for n in CACHE), tokens=sum(qlens), max_q=m, kv_format="int8")
+         for m in (max(qlens), 2**31 - 1)]
+    assert torch.equal(k[0][0], k[1][0]) and torch.equal(k[0][1], k[1][1])
+    assert ea.device_status() == 0
+
+
 def test_many_splits_join():
     # Long keys whose parts differ by far in weight: the last keys' scores dominate.
     st = make([3], [6000], 4, 1, 128, "e4m3", seed=19)
