@@ -34,12 +34,15 @@
 //  * Exactness.  Codes are exact in f16.  Queries are scaled by a power of two
 //    per row before rounding to f16, exact for elements within 2^28 of the
 //    row's largest.  The K scale multiplies the f32 scores, per page.  The V
-//    scale, relative to a power of two below the largest V scale of the CTA's
-//    pages, multiplies P in f32 before it is rounded to f16 (2^-11 of each,
-//    against bf16's 2^-8 of the output).  (Terms under 2^-19 of the largest V
-//    scale times the row's largest P lose bits.  Scaling the codes on their way
-//    instead costs two roundings, and as much time: 600 us for the 16 chunks
-//    either way, in a run long enough for the power limit.)
+//    scale multiplies P in f32 before it is rounded to f16 (2^-11 of each, against
+//    bf16's 2^-8 of the output), relative to the largest of the row's own
+//    contributions so far, P times V scale over the keys that it sees: what it does
+//    not see, and what it barely attends, moves nothing.  (Terms under 2^-18 of
+//    that largest one lose bits, 2^-29 of it at most.  Relative to the largest V
+//    scale of the CTA's pages, one later large value took the bits of every row
+//    before it; that took 561 us for the 16 chunks above, 945 with ALiBi and 481
+//    with d = 64, this 566, 954 and 490.  Scaling the codes on their way
+//    costs two roundings, and as much time.)
 //  * Few rows and long keys.  A chunk that fits one row tile gives both tiles the
 //    same rows and half of the CTA's keys each ("twin"), which overlaps what one
 //    tile alone does in turn: 146 us -> 89 us for the 20 rows above, with the
@@ -83,6 +86,7 @@ constexpr int CHUNK_BYTES = 128 * 128;  // one 128-row x 128-byte swizzle column
 constexpr int kSMs = 148;
 constexpr int kScaleRing = 8;  // tiles whose page scales are kept in shared memory
 constexpr int kEdge = 4;       // tiles that a row may see in part, at either end of the walk
+constexpr float kTop = 4.f;    // log2 of what a row's reference contribution is in f16
 
 template <int D, bool kTwin>
 struct Cfg {
@@ -93,8 +97,7 @@ struct Cfg {
   static constexpr int NRAW = 4;                 // raw slots
   static constexpr int RING_OFF = NQ * TILE_BYTES;
   static constexpr int RAW_OFF = RING_OFF + NST * TILE_BYTES;
-  static constexpr int XFER_OFF = RAW_OFF + NRAW * RAW_BYTES;  // twin: m and l of tile 1's rows
-  static constexpr int BAR_OFF = XFER_OFF + (kTwin ? 1024 : 0);
+  static constexpr int BAR_OFF = RAW_OFF + NRAW * RAW_BYTES;
   static constexpr int SMEM_BYTES = BAR_OFF + 1024 + 1024;  // + 1 KB align slack
   static constexpr uint32_t IDESC_QK =  // as idesc_bf16_f32, with both operand formats 0 (f16)
       idesc_bf16_f32(BM, BN, false, false) & ~((7u << 7) | (7u << 10));
@@ -112,14 +115,12 @@ struct Shared {
   uint64_t p_full[2];
   uint64_t o_half[2];
   uint64_t o_full[2];
-  uint64_t mrg_full;  // twin: tile 1's m and l are published
+  uint64_t mrg_full;  // twin: what tile 1 knows of its rows is published
   uint64_t mma_done;
   alignas(16) float k_scale[kScaleRing][kPagesPerTile];
   alignas(16) float v_scale[kScaleRing][kPagesPerTile];
   unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with a code that is no number
-  unsigned v_top;                      // largest finite |V scale| of the CTA's pages, as bits
   int any_bad;
-  unsigned poison1[BM / 32];  // twin: rows of tile 1 that see a value left out
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -205,8 +206,8 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &a, uint32_t &b) {
 }
 
 // N columns of a score row -> N / 2 f16 pairs of P = 2^(s*c - m), c
-// the multiplier of the columns' page, times their page's V scale v; returns the
-// part of the row sum, which has no V scale.
+// the multiplier of the columns' page, times their page's weight v; returns the
+// part of the row sum, which has no weights.
 template <int N>
 __device__ __forceinline__ float exp_cols(const uint32_t (&sv)[N], const float *c, const float *v,
                                           float m, uint32_t (&pk)[N / 2]) {
@@ -231,6 +232,56 @@ __device__ __forceinline__ float exp_cols(const uint32_t (&sv)[N], const float *
 }
 __device__ __forceinline__ void store_half(uint32_t addr, const uint32_t (&pk)[32]) {
   tmem_st32(addr, pk);
+}
+// Four columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d))
+               : "memory");
+}
+__device__ __forceinline__ float4 tmem_ld4(uint32_t addr) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
+  return make_float4(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]), __uint_as_float(r[3]));
+}
+
+// A row's references, log2: m of its scaled scores, for the sum of P, and mv of its
+// contributions, scores plus log2 |V scale| of the keys it sees, for P V.  The
+// weight of a page's P in f16 is V scale * 2^(m - mv + kTop), taken as two factors
+// h: far scales can put the whole outside float32.
+__device__ __forceinline__ float half_weight(float m, float mv) {
+  return m == -INFINITY ? 0.f : ex2(0.5f * (m - mv + kTop));
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.4028235e38f; }
+// log2 |V scale| for the references, at least that of the smallest normal number (a
+// page of zeros contributes nothing, but its rows need a finite reference); that
+// too for a scale that is no number, whose page counts as zeros.
+__device__ __forceinline__ float scale_log2(float v) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fabsf(v)));
+  return finite(v) ? fmaxf(y, -126.f) : -126.f;
+}
+// Weights of N pages against a row's references, from their V scales v; visible
+// columns [lo, hi).  Where a scale is no number its page weighs nothing and a row
+// that sees it is poisoned.  A weight beyond float32 becomes its largest: P is 0 in
+// float32 there, or the reference would have moved.  (Without a branch: one around
+// the rare part cost 2 % of the time of 16 chunks of 512.)
+template <int N>
+__device__ __forceinline__ void weigh(float (&v)[N], float h, int lo, int hi, bool &poison) {
+  const float2 h2 = make_float2(h, h), z2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int g = 0; g < N; g += 2) {
+    const float2 x = fma2(fma2(make_float2(v[g], v[g + 1]), h2, z2), h2, z2);
+    const float w[2] = {x.x, x.y};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool number = finite(v[g + k]);
+      poison |= !number && lo < kPage * (g + k + 1) && hi > kPage * (g + k);
+      v[g + k] = number ? fminf(fmaxf(w[k], -3.4028235e38f), 3.4028235e38f) : 0.f;
+    }
+  }
 }
 
 // A sequence's chunk: rows q0 .. q0 + nq - 1, its last token the n-th.  False
@@ -440,7 +491,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
   const int rows_here = min(p.span, ck.nq - tok0) * p.heads;
   const bool few = kTwin && rows_here <= 32;
 
-  // ---- every page of those tiles must be in the pool; and their largest V scale.
+  // ---- every page of those tiles must be in the pool.
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&sh->full[i], 128);
@@ -458,7 +509,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     mbar_init(&sh->mma_done, 1);
     sh->abort_flag = 0;
     sh->any_bad = 0;
-    sh->v_top = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < 2 * kEdge * (BN / 32)) (&sh->v_bad[0][0])[threadIdx.x] = 0;
@@ -466,18 +516,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
   {
     const int pg_end = min(jhi * kPagesPerTile, (ck.n + kPage - 1) / kPage);
     bool bad = false;
-    unsigned top = 0;
     for (int i = jlo * kPagesPerTile + static_cast<int>(threadIdx.x); i < pg_end; i += NUM_THREADS) {
       const int pid = p.block_table[static_cast<size_t>(seq) * p.max_blocks + i];
-      if (pid < 0 || pid >= p.num_pages) {
-        bad = true;
-      } else {
-        const unsigned u = __float_as_uint(p.v_scales[static_cast<size_t>(pid) * p.Hkv + hkv]) & 0x7fffffffu;
-        if (u < 0x7f800000u) top = max(top, u);
-      }
+      bad |= pid < 0 || pid >= p.num_pages;
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0 && top) atomicMax(&sh->v_top, top);
     if (__syncthreads_or(bad) || jlo >= jhi) {
       // NaN rows for a bad page; nothing (weight zero) for a part without keys.
       const bool none = jlo >= jhi;
@@ -507,10 +549,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
-  // V is widened relative to 2^v_exp: the largest scale lands in [2^5, 2^6), so
-  // that 448 of it stays below f16's largest.
-  int v_exp = 0;
-  if (sh->v_top) v_exp = max(-120, static_cast<int>(sh->v_top >> 23) - 127 - 5);
 
   if (warp < 4) {
     // ================================================================== MMA
@@ -681,7 +719,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     // Numbers are read two rounds ahead and scales one, so that neither's latency
     // is waited for.
     const int *table = p.block_table + static_cast<size_t>(seq) * p.max_blocks;
-    const float v_unit = __uint_as_float(static_cast<uint32_t>(127 - v_exp) << 23);
     auto page_of = [&](int i0) {
       const int i = i0 + (lane >> 1);
       if (i >= total) return -1;
@@ -700,7 +737,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       if (v) return x;
       const size_t slice = static_cast<size_t>(pid) * p.Hkv + hkv;
       x.x = p.k_scales[slice];
-      x.y = p.v_scales[slice] * v_unit;
+      x.y = p.v_scales[slice];
       return x;
     };
     int pid = page_of(0), pid1 = page_of(16);  // of entry i's round, and the next
@@ -850,9 +887,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     const float slope2 = kAlibi && valid ? p.slopes[hq] * 1.4426950408889634f : 0.f;
     // A warp without a row of its own (a chunk of a few tokens) only hands on.
     const bool idle = !__any_sync(0xffffffffu, valid);
-    float m = -INFINITY;  // reference max, in log2 units of scaled scores
+    float m = -INFINITY, mv = -INFINITY;  // references (see half_weight)
+    float h = 0.f;                        // half_weight(m, mv)
     float l = 0.f;
-    bool poison = false;  // the row sees a value that is no number and was left out
+    bool poison = false;  // the row sees a V scale that is no number, or a value left out
     bool ok = true;
     if (few) {
       // The softmax of this thread's row over columns 32 * quarter .. of every
@@ -874,33 +912,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         const float2 ks = *reinterpret_cast<const float2 *>(&sh->k_scale[slot][2 * quarter]);
         const float2 vs = *reinterpret_cast<const float2 *>(&sh->v_scale[slot][2 * quarter]);
         const float cp[2] = {ks.x * c_row, ks.y * c_row};
-        float vp[2] = {vs.x, vs.y};
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          if (!(fabsf(vp[g]) <= 3.4028235e38f)) {
-            poison |= lo < kPage * (g + 1) && hi > kPage * g;
-            vp[g] = 0.f;
-          }
         tmem_ld_wait(sv);
         const float rb = kAlibi ? slope2 * static_cast<float>(j * BN + c0 - (ck.ctx + tok)) : 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY;
+        float m0 = -INFINITY, m1 = -INFINITY;  // of either page
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
+        for (int i = 0; i < kPage; ++i) {
 #pragma unroll
-          for (int k = i; k < i + 2; ++k) {
+          for (int k = i; k < 2 * kPage; k += kPage) {
             float x = __uint_as_float(sv[k]) * cp[k / kPage];
             if (kAlibi) x += fmaf(slope2, static_cast<float>(k), rb);
             if (masked && (k < lo || k >= hi)) x = -INFINITY;
             sv[k] = __float_as_uint(x);
           }
           m0 = fmaxf(m0, __uint_as_float(sv[i]));
-          m1 = fmaxf(m1, __uint_as_float(sv[i + 1]));
+          m1 = fmaxf(m1, __uint_as_float(sv[i + kPage]));
         }
         const float m_new = fmaxf(m, fmaxf(m0, m1));
-        const bool resc = m_new > m + 8.0f;
-        const float alpha = resc ? ex2(m - m_new) : 1.0f;
-        if (resc) m = m_new;
-        l *= alpha;
+        const float mv_new = fmaxf(mv, fmaxf(m0 + scale_log2(vs.x), m1 + scale_log2(vs.y)));
+        if (m_new > m + 8.0f) {
+          l *= ex2(m - m_new);
+          m = m_new;
+        }
+        const bool resc = mv_new > mv + 8.0f;
+        const float alpha = resc ? ex2(mv - mv_new) : 1.0f;
+        if (resc) mv = mv_new;
         if (jj > 0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
@@ -912,6 +947,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
             tmem_st32(o_addr + cc * 32, ov);
           }
         }
+        float vp[2] = {vs.x, vs.y};
+        weigh(vp, half_weight(m, mv), lo, hi, poison);
         const float ones[2] = {1.f, 1.f};
         l += exp_cols(sv, ones, vp, m == -INFINITY ? 0.f : m, pk);
         const uint32_t zero[16] = {};
@@ -943,47 +980,48 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         continue;
       }
       tc_fence_after();
+      const int slot = (kTwin ? 2 * jj + t : j - jlo) % kScaleRing;
       // The multipliers of each page's columns.
       float cp[kPagesPerTile];
       {
-        const float4 *ks = reinterpret_cast<const float4 *>(sh->k_scale[(kTwin ? 2 * jj + t : j - jlo) % kScaleRing]);
+        const float4 *ks = reinterpret_cast<const float4 *>(sh->k_scale[slot]);
         const float4 a = ks[0], b = ks[1];
         cp[0] = a.x * c_row; cp[1] = a.y * c_row; cp[2] = a.z * c_row; cp[3] = a.w * c_row;
         cp[4] = b.x * c_row; cp[5] = b.y * c_row; cp[6] = b.z * c_row; cp[7] = b.w * c_row;
       }
-      // The V scales, which P takes here.
-      float vp[kPagesPerTile];
-      {
-        const float4 *vs = reinterpret_cast<const float4 *>(sh->v_scale[(kTwin ? 2 * jj + t : j - jlo) % kScaleRing]);
-        const float4 a = vs[0], b = vs[1];
-        vp[0] = a.x; vp[1] = a.y; vp[2] = a.z; vp[3] = a.w;
-        vp[4] = b.x; vp[5] = b.y; vp[6] = b.z; vp[7] = b.w;
-        const float any = (vp[0] + vp[1] + vp[2] + vp[3]) + (vp[4] + vp[5] + vp[6] + vp[7]);
-        if (!(fabsf(any) <= 3.4028235e38f)) {
-          // A scale that is no number: rows that see its page get NaN, and no
-          // zero P is multiplied by it.
-#pragma unroll
-          for (int g = 0; g < kPagesPerTile; ++g)
-            if (!(fabsf(vp[g]) <= 3.4028235e38f)) {
-              poison |= lo < kPage * (g + 1) && hi > kPage * g;
-              vp[g] = 0.f;
-            }
-        }
-      }
+      auto four = [](const float *at, float *to) {
+        const float4 a = *reinterpret_cast<const float4 *>(at);
+        to[0] = a.x; to[1] = a.y; to[2] = a.z; to[3] = a.w;
+      };
       // The row goes in halves of 64 columns, and the first half's P is handed
       // on while the second is worked on.  P of columns 0-63 lies over S columns
       // 0-31, that of 64-127 over 32-63.
       uint32_t sv[64], pk[32];
       bool first_done = false;  // the first half's P is out, against m as it was
       if (attempt) {
-        // An unmasked tile first takes P against the running reference as it
-        // stands, without looking for its own max.  Where a half's sum is at
-        // most 255 in every row, each of its terms is below 2^8 and the
-        // max-first step below would have kept the reference too.
+        // An unmasked tile first takes P against the running references as they
+        // stand, without looking for its own.  Where a half's sum is at most 255
+        // in every row, each of its terms is below 2^8 and the max-first step
+        // below would have kept m too; and where that times the weights' sum is at
+        // most 2^15 (and so no NaN), no product passes f16's largest.
         tmem_ld64(s_addr, sv);
+        // The V scales, which P takes here, as weights against the references.
+        float vp[kPagesPerTile];
+        four(&sh->v_scale[slot][0], vp);
+        four(&sh->v_scale[slot][4], vp + 4);
+#pragma unroll
+        for (int g = 0; g < kPagesPerTile; g += 2) {
+          const float2 h2 = make_float2(h, h), z2 = make_float2(0.f, 0.f);
+          const float2 x = fma2(fma2(make_float2(vp[g], vp[g + 1]), h2, z2), h2, z2);
+          vp[g] = x.x;
+          vp[g + 1] = x.y;
+        }
+        const float all = ((fabsf(vp[0]) + fabsf(vp[1])) + (fabsf(vp[2]) + fabsf(vp[3]))) +
+                          ((fabsf(vp[4]) + fabsf(vp[5])) + (fabsf(vp[6]) + fabsf(vp[7])));
+        auto fits = [&](float sum) { return sum <= 255.0f && sum * all <= 32768.0f; };
         tmem_ld_wait64(sv);
         const float l0 = exp_cols(sv, cp, vp, m, pk);
-        if (__all_sync(0xffffffffu, l0 <= 255.0f)) {
+        if (__all_sync(0xffffffffu, fits(l0))) {
           first_done = true;
           tmem_ld64(s_addr + 64, sv);
           store_half(s_addr, pk);
@@ -993,7 +1031,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
           l += l0;
           tmem_ld_wait64(sv);
           const float l1 = exp_cols(sv, cp + 4, vp + 4, m, pk);
-          if (__all_sync(0xffffffffu, l1 <= 255.0f)) {
+          if (__all_sync(0xffffffffu, fits(l1))) {
             l += l1;
             store_half(s_addr + 32, pk);
             tmem_st_wait();
@@ -1007,42 +1045,47 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       // To scaled scores (log2 units) with the bias; masked ones to -inf,
       // whatever they were.
       const float rb = kAlibi ? slope2 * static_cast<float>(j * BN - (ck.ctx + tok)) : 0.f;
-      auto scaled_half = [&](int h) {
-        tmem_ld64(s_addr + 64 * h, sv);
+      auto scaled_half = [&](int hf) {
+        tmem_ld64(s_addr + 64 * hf, sv);
         tmem_ld_wait64(sv);
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          float x = __uint_as_float(sv[i]) * (h ? cp[4 + i / kPage] : cp[i / kPage]);
-          if (kAlibi) x += fmaf(slope2, static_cast<float>(64 * h + i), rb);
+          float x = __uint_as_float(sv[i]) * (hf ? cp[4 + i / kPage] : cp[i / kPage]);
+          if (kAlibi) x += fmaf(slope2, static_cast<float>(64 * hf + i), rb);
           sv[i] = __float_as_uint(x);
         }
         if (masked) {
-          const int lo_h = lo - 64 * h, hi_h = hi - 64 * h;
+          const int lo_h = lo - 64 * hf, hi_h = hi - 64 * hf;
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (i < lo_h || i >= hi_h) sv[i] = 0xff800000u;
         }
       };
-      auto half_max = [&]() {
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          m0 = fmax3(m0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-          m1 = fmax3(m1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
-        }
-        return fmaxf(m0, m1);
-      };
-      float m_new = m;
+      float m_new = m, mv_new = mv;
 #pragma unroll 1
-      for (int h = first_done; h < 2; ++h) {
-        scaled_half(h);
-        m_new = fmaxf(m_new, half_max());
+      for (int hf = first_done; hf < 2; ++hf) {
+        scaled_half(hf);
+        float vp[4];
+        four(&sh->v_scale[slot][4 * hf], vp);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {  // a page's columns
+          float top = fmaxf(__uint_as_float(sv[16 * g]), __uint_as_float(sv[16 * g + 1]));
+#pragma unroll
+          for (int i = 16 * g + 2; i < 16 * g + 16; i += 2)
+            top = fmax3(top, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+          m_new = fmaxf(m_new, top);
+          mv_new = fmaxf(mv_new, top + scale_log2(vp[g]));
+        }
       }
-      // The reference moves where it must (by 2^8 or more), and after a miss.
-      const bool resc = m_new > m + 8.0f || (attempt && m_new > m);
-      const float alpha = resc ? ex2(m - m_new) : 1.0f;
-      if (resc) m = m_new;
-      l *= alpha;
+      // The references move where they must (by 2^8 or more), and after a miss.
+      if (m_new > m + 8.0f || (attempt && m_new > m)) {
+        l *= ex2(m - m_new);
+        m = m_new;
+      }
+      const bool resc = mv_new > mv + 8.0f || (attempt && mv_new > mv);
+      const float alpha = resc ? ex2(mv - mv_new) : 1.0f;
+      if (resc) mv = mv_new;
+      h = half_weight(m, mv);
       if (jj > 0 && __any_sync(0xffffffffu, resc)) {
         // Lazy rescale of O.  S(j) being there implies that PV(j-1) is done; of
         // PV(j), the first half may be under way if its P is out.
@@ -1067,14 +1110,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       const float m_use = (m == -INFINITY) ? 0.f : m;
       const float ones[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll 1
-      for (int h = first_done; h < 2; ++h) {
-        scaled_half(h);
-        const float vh[4] = {h ? vp[4] : vp[0], h ? vp[5] : vp[1], h ? vp[6] : vp[2], h ? vp[7] : vp[3]};
-        l += exp_cols(sv, ones, vh, m_use, pk);
-        store_half(s_addr + 32 * h, pk);
+      for (int hf = first_done; hf < 2; ++hf) {
+        scaled_half(hf);
+        float vp[4];
+        four(&sh->v_scale[slot][4 * hf], vp);
+        weigh(vp, h, lo - 64 * hf, hi - 64 * hf, poison);
+        l += exp_cols(sv, ones, vp, m_use, pk);
+        store_half(s_addr + 32 * hf, pk);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(h ? &sh->p_full[t] : &sh->p_half[t]);
+        mbar_arrive(hf ? &sh->p_full[t] : &sh->p_half[t]);
       }
     }
     if (ok && nt > 0) {
@@ -1113,7 +1158,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         if (x.y != 0.f) sum += x.y * ex2(x.x - mm);
       }
       const bool use = ok && nt > 0 && l != 0.f;
-      const float weight = use ? ex2(m - mm) * (poison ? NAN : scalbnf(1.0f / sum, v_exp)) : 0.f;
+      // O is relative to 2^(mv - kTop); in two factors, as that may be far from 1.
+      const float part = ex2(0.5f * (mv - mm - kTop)), last = part * (poison ? NAN : 1.0f / sum);
       constexpr int kRow = D + 4;  // floats; keeps a store's eight lanes in different banks
       float *joint = reinterpret_cast<float *>(sRing + 8 * 32 * sizeof(float4));
       tc_fence_after();
@@ -1127,7 +1173,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         for (int i = 0; i < 32; i += 4) {
           float x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = use ? __uint_as_float(ov[i + k]) * weight : 0.f;
+          for (int k = 0; k < 4; ++k) x[k] = use ? __uint_as_float(ov[i + k]) * part * last : 0.f;
           dst[i >> 2] = make_float4(x[0], x[1], x[2], x[3]);
         }
       }
@@ -1156,18 +1202,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       ok = false;  // nothing more for these warps
     }
     // (l != 0 for a NaN too; 0 for a row that saw no key here: part of them only.)
-    float a0 = l != 0.f ? 1.f : 0.f, a1 = 0.f;  // weights of the O tiles
+    bool use0 = nt > 0 && l != 0.f, use1 = false;  // the O tiles that count
+    float mv1 = 0.f;
     if (kTwin && !few) {
       // The tiles hold partial results of the same rows over disjoint keys: tile
-      // 1's threads publish their m and l, and tile 0's join them.
-      float2 *xfer = reinterpret_cast<float2 *>(smem + C::XFER_OFF);
+      // 1's threads publish what they know of their rows in the first columns of
+      // its S, which nothing needs any more, and tile 0's, whose lanes are the
+      // same, join them.
       if (t == 1) {
         if (ok) {
-          xfer[r] = make_float2(m, l);
-          const unsigned rows = __ballot_sync(0xffffffffu, poison);
-          if (lane == 0) sh->poison1[quarter] = rows;
+          tmem_st4(s_addr, m, l, mv, poison ? 1.f : 0.f);
+          tmem_st_wait();
           tc_fence_before();
-          __syncwarp();
           mbar_arrive(&sh->mrg_full);
         }
         ok = false;  // nothing more for this warpgroup
@@ -1175,24 +1221,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         ok = __all_sync(0xffffffffu, mbar_wait(&sh->mrg_full, 0, abort_flag, p.status));
         if (ok) {
           tc_fence_after();
-          const float2 x = xfer[r];
+          const float4 x = tmem_ld4(s_addr + 128);
           const float mm = fmaxf(m, x.x);
-          a0 = l != 0.f ? ex2(m - mm) : 0.f;
-          a1 = x.y != 0.f ? ex2(x.x - mm) : 0.f;
-          l = (l != 0.f ? a0 * l : 0.f) + (x.y != 0.f ? a1 * x.y : 0.f);
+          use1 = x.y != 0.f;
+          l = (use0 ? ex2(m - mm) * l : 0.f) + (use1 ? ex2(x.x - mm) * x.y : 0.f);
           m = mm;
-          poison |= (sh->poison1[quarter] >> lane & 1u) != 0;
+          mv1 = x.z;
+          poison |= x.w != 0.f;
         }
       }
     }
     if (ok && (nt > 0 || p.split)) {
       tc_fence_after();
       const bool seen = l != 0.f;
-      const float inv = poison ? NAN : (seen ? scalbnf(1.0f / l, v_exp) : 0.f);
+      const float inv = poison ? NAN : (seen ? 1.0f / l : 0.f);
       const float l2 = seen ? m + log2f(l) : -INFINITY;
-      const bool use0 = nt > 0 && a0 != 0.f, use1 = kTwin && a1 != 0.f;
-      a0 *= inv;
-      a1 *= inv;
+      // O is relative to 2^(mv - kTop); in two factors, as that may be far from 1.
+      const float a0 = ex2(0.5f * (mv - m - kTop)), a1 = ex2(0.5f * (mv1 - m - kTop));
+      const float b0 = a0 * inv, b1 = a1 * inv;
       const size_t prow = static_cast<size_t>(lin) * p.rows_cap + (kTwin ? 0 : t * p.tokens * p.heads) + r;
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
@@ -1204,8 +1250,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         // (A tile that has seen nothing may hold anything.)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          float x = use0 ? __uint_as_float(ov[i]) * a0 : 0.f;
-          if constexpr (kTwin) x += use1 ? __uint_as_float(ov1[i]) * a1 : 0.f;
+          float x = use0 ? __uint_as_float(ov[i]) * a0 * b0 : 0.f;
+          if constexpr (kTwin) x += use1 ? __uint_as_float(ov1[i]) * a1 * b1 : 0.f;
           ov[i] = __float_as_uint(x);
         }
         if (valid && !p.split) {

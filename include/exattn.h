@@ -367,9 +367,10 @@ EXATTN_API attn_status_t attn_kv_read_paged_q8(
  *                where that is 0.  Calls that may run at the same time need one
  *                each.
  * Inside the kernel queries are rounded to f16 after a per-row power-of-two
- * normalisation, and P times the V scale to f16, relative to the largest V scale
- * of the keys at hand (terms 2^-19 of it and smaller lose bits); scores, sums and
- * outputs accumulate in float32.
+ * normalisation, and P times the V scale to f16, relative to the row's largest
+ * such product (2^-11 of each, or 2^-29 of the largest where that is more): values
+ * of keys that a row does not see have no part in it, however large.  Scores, sums
+ * and outputs accumulate in float32.
  */
 EXATTN_API size_t attn_prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q, int d,
                                                   int max_blocks, int page_size);
