@@ -41,7 +41,7 @@
 //    that largest one lose bits, 2^-29 of it at most.  Relative to the largest V
 //    scale of the CTA's pages, one later large value took the bits of every row
 //    before it; that took 561 us for the 16 chunks above, 945 with ALiBi and 481
-//    with d = 64, this 566, 954 and 490.  Scaling the codes on their way
+//    with d = 64, this 567, 952 and 485.  Scaling the codes on their way
 //    costs two roundings, and as much time.)
 //  * Few rows and long keys.  A chunk that fits one row tile gives both tiles the
 //    same rows and half of the CTA's keys each ("twin"), which overlaps what one
@@ -55,7 +55,9 @@
 //  * NaN behind the mask: a masked score is replaced, whatever it was.  In the
 //    P V product a zero weight would not cancel a NaN value, so in tiles that
 //    some row sees only in part such values enter as zeros and are noted by
-//    key; a row that does see a noted key gets NaN.
+//    key; a row that does see a noted key gets NaN in the elements it has one in,
+//    as the product gives in the other tiles.  A V scale that is no number makes
+//    every element NaN in the rows that see its page.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -119,8 +121,9 @@ struct Shared {
   uint64_t mma_done;
   alignas(16) float k_scale[kScaleRing][kPagesPerTile];
   alignas(16) float v_scale[kScaleRing][kPagesPerTile];
-  unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with a code that is no number
+  unsigned v_bad[2 * kEdge][BN / 32];  // keys of edge tiles with codes that are no numbers
   int any_bad;
+  int seq, hkv, edge_hi, edge_0, jlo, jhi;  // of the CTA, for the epilogue's rare reader
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -509,6 +512,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     mbar_init(&sh->mma_done, 1);
     sh->abort_flag = 0;
     sh->any_bad = 0;
+    sh->seq = seq;
+    sh->hkv = hkv;
+    sh->edge_hi = edge_hi;
+    sh->edge_0 = edge_0;
+    sh->jlo = jlo;
+    sh->jhi = jhi;
     fence_mbar_init();
   }
   if (threadIdx.x < 2 * kEdge * (BN / 32)) (&sh->v_bad[0][0])[threadIdx.x] = 0;
@@ -890,7 +899,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     float m = -INFINITY, mv = -INFINITY;  // references (see half_weight)
     float h = 0.f;                        // half_weight(m, mv)
     float l = 0.f;
-    bool poison = false;  // the row sees a V scale that is no number, or a value left out
+    bool poison = false;  // the row sees a page whose V scale is no number
     bool ok = true;
     if (few) {
       // The softmax of this thread's row over columns 32 * quarter .. of every
@@ -1126,17 +1135,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       ok = mbar_wait(&sh->o_full[t], (nt - 1) & 1, abort_flag, p.status);
       ok = __all_sync(0xffffffffu, ok);
     }
-    // Codes that are no numbers were left out of the edge tiles: rows that see
-    // their keys get NaN.
-    if (ok && nt > 0 && *reinterpret_cast<volatile int *>(&sh->any_bad)) {
+    // Codes that are no numbers were left out of the edge tiles: the elements that
+    // they make NaN in the row of token tk, stored as row `at`, are written over, by
+    // reading the row's keys that have one again.  (In the other tiles, which every
+    // row sees whole, the product does it.  What this needs of the CTA waits in
+    // shared memory: held in registers through the softmax it took every call 2 %.)
+    auto spoil = [&](int tk, size_t at) {
+      const volatile Shared *cta = sh;
+      const int pos = ck.ctx + tk;
+#pragma unroll 1
       for (int e = 0; e < 2 * kEdge; ++e) {
-        const int j = e < kEdge ? edge_hi + e : edge_0 + e - kEdge;
-        if (j < jst || j >= jen || (e >= kEdge && j >= edge_hi)) continue;
-        const int hi = min(BN, ck.ctx + tok - j * BN + 1);
-        const int lo = p.window > 0 ? max(0, ck.ctx + tok - p.window + 1 - j * BN) : 0;
-        for (int i = lo; i < hi; ++i) poison |= (sh->v_bad[e][i >> 5] >> (i & 31) & 1u) != 0;
+        const int j = e < kEdge ? cta->edge_hi + e : cta->edge_0 + e - kEdge;
+        if (j < cta->jlo || j >= cta->jhi || (e >= kEdge && j >= cta->edge_hi)) continue;
+        const int hi = min(BN, pos - j * BN + 1);
+        const int lo = p.window > 0 ? max(0, pos - p.window + 1 - j * BN) : 0;
+#pragma unroll 1
+        for (int i = lo; i < hi; ++i) {
+          if (!(cta->v_bad[e][i >> 5] >> (i & 31) & 1u)) continue;
+          const int key = j * BN + i;
+          const int pid = p.block_table[static_cast<size_t>(cta->seq) * p.max_blocks + key / kPage];
+          const uint8_t *code = p.v_pages + ((static_cast<size_t>(pid) * p.Hkv + cta->hkv) * kPage + key % kPage) * D;
+#pragma unroll 1
+          for (int c = 0; c < D; ++c) {
+            if ((code[c] & 0x7fu) != 0x7fu) continue;
+            if (p.split) p.o_part[at * D + c] = NAN;
+            else p.o[at * D + c] = __float2bfloat16_rn(NAN);
+          }
+        }
       }
-    }
+    };
     if (few) {
       // Eight partial results of every row, over disjoint keys: joined through
       // the ring, which is free once both tiles' products are done.
@@ -1198,6 +1225,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         const float l2 = sum != 0.f ? mm + log2f(sum) : -INFINITY;
         if (!p.split) p.lse[out_row] = l2 * 0.6931471805599453f;
         else p.l2_part[static_cast<size_t>(lin) * p.rows_cap + lane] = l2;
+      }
+      if (FMT == ATTN_KV_E4M3 && *reinterpret_cast<volatile int *>(&sh->any_bad)) {
+        soft_barrier();  // the rows are stored
+        if (me == 0 && valid) spoil(tok, p.split ? static_cast<size_t>(lin) * p.rows_cap + lane : out_row);
       }
       ok = false;  // nothing more for these warps
     }
@@ -1273,6 +1304,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       if (valid) {
         if (!p.split) p.lse[out_row] = l2 * 0.6931471805599453f;
         else p.l2_part[prow] = l2;
+        if (FMT == ATTN_KV_E4M3 && *reinterpret_cast<volatile int *>(&sh->any_bad)) spoil(tok, p.split ? prow : out_row);
       }
     }
   }

@@ -359,8 +359,9 @@ EXATTN_API attn_status_t attn_kv_read_paged_q8(
  * bad pages as for attn_prefill_paged; pages, scales and kv_format as for
  * attn_decode_paged_q8 (the chunk's own tokens have been written, e.g. by
  * attn_kv_write_paged_q8).  Rows of no sequence stay as they are.
- * A value of V that is no finite number reaches every element of the rows that
- * see its token, and only those.
+ * A code of V that is NaN makes its element of O NaN in the rows that see its
+ * token, and a V scale that is not finite every element in the rows that see a
+ * token of its page; nothing else changes.
  *
  *   workspace    device scratch of at least attn_prefill_q8_workspace_bytes(...)
  *                bytes, owned by the caller; no initialisation needed, NULL

@@ -144,3 +144,40 @@ def test_scales_of_zero(nq, copies):
     st["v_scales"][:] = 0.0
     o, lse = run(on_gpu(st), "e4m3")
     assert not o.any() and lse.isfinite().all()
+
+
+@pytest.mark.parametrize("nq,copies", [(5, 0), (5, 80), (60, 0), (60, 80), (300, 0), (300, 80)])
+@pytest.mark.parametrize("window", [0, 40, 500])
+def test_a_code_that_is_no_number_reaches_its_element_only(nq, copies, window):
+    # NaN codes of V, one at a time: in tiles that every row sees whole, at the window's ends, on
+    # the diagonal, in the last page.  Rows that see the token get NaN in that element of O.
+    ctx, fmt = 1000, "e4m3"
+    n = ctx + nq
+    st = sequences(nq, ctx, copies, fmt, seed=nq + window)
+    want = reference(st, fmt, window)
+    pos = ctx + np.arange(nq)
+    toks = [3, 300, ctx - 300, ctx - 20, ctx, ctx + nq // 2, n - 1]
+    if window:
+        toks += [ctx - window, ctx - window + 1, ctx - window + nq // 2, n - window]
+    for i, tok in enumerate(toks):
+        col = (5, 40, 63, 0)[i % 4]
+        sick = dict(st, v_pages=st["v_pages"].clone())
+        p = int(st["block_table"][0, tok // 16])
+        sick["v_pages"].view(torch.uint8)[p, 1, tok % 16, col] = (0x7F, 0xFF)[i % 2]
+        o, lse = run(on_gpu(sick), fmt, window=window)
+        hit = (pos >= tok) & ((pos - window < tok) if window else True)
+        nan = np.zeros((nq, HQ, D), bool)
+        nan[hit, HQ // HKV:, col] = True
+        got = f64(o)[:nq]
+        assert np.array_equal(np.isnan(got), nan), tok
+        lim = 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -10.6 * want[2]
+        assert (np.abs(got - want[0]) <= lim)[~nan].all(), tok
+        assert (np.abs(f64(lse)[:nq] - want[1]) <= 2.0 ** -13 + 2.0 ** -20 * np.abs(want[1])).all()
+    # Several at once, two of them in one element, one in a page of its own.
+    sick = dict(st, v_pages=st["v_pages"].clone())
+    nan = np.zeros((nq, HQ, D), bool)
+    for tok, col in ((ctx, 7), (ctx + nq // 2, 7), (n - 1, 8), (ctx - 20, 33), (3, 34)):
+        sick["v_pages"].view(torch.uint8)[int(st["block_table"][0, tok // 16]), 0, tok % 16, col] = 0x7F
+        hit = (pos >= tok) & ((pos - window < tok) if window else True)
+        nan[hit, :HQ // HKV, col] = True
+    assert np.array_equal(np.isnan(f64(run(on_gpu(sick), fmt, window=window)[0])[:nq]), nan)
