@@ -366,7 +366,7 @@ attn_status_t attn_kv_read_paged_q8(
 size_t attn_prefill_q8_workspace_bytes(int S, int Hq, int Hkv, int T, int max_q, int d,
                                        int max_blocks, int page_size) {
   if (S <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || T <= 0 || max_q <= 0 || max_blocks <= 0 ||
-      page_size != 16 || (d != 64 && d != 128))
+      page_size != 16 || (d != 64 && d != 128) || static_cast<long long>(T) * Hq >= (1LL << 31))
     return 0;
   return prefill_q8_workspace_bytes(S, Hq, Hkv, T, std::min(max_q, T), d, max_blocks);
 }

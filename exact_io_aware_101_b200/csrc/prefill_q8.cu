@@ -1371,9 +1371,9 @@ struct Cut {
 Cut cut(int S, int Hq, int Hkv, int max_q, int max_blocks) {
   Cut c;
   const int G = Hq / Hkv;
-  int n = (G + BM - 1) / BM;  // the fewest equal head groups of at most 128
-  while (G % n) ++n;
-  c.heads = G / n;
+  c.heads = G < BM ? G : BM;  // the fewest equal head groups of at most 128
+  while (G % c.heads) --c.heads;
+  const int n = G / c.heads;
   c.tokens = BM / c.heads;
   const bool many = max_blocks > kPagesPerTile;  // more than one key tile
   // Chunks that fit one row tile: both tiles take the same rows and half the
