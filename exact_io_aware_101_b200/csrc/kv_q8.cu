@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 
 // Four floats to four codes (element 0 in the low byte), rounded to nearest
-// even.  E4M3 saturates at 448; INT8 takes |q| below 127.5.
+// even.  E4M3 saturates at 448; INT8 takes -128.5 < q < 127.5.
 template <int FMT>
 __device__ __forceinline__ uint32_t codes4(const float *q) {
   if constexpr (FMT == ATTN_KV_E4M3) {
@@ -115,7 +115,9 @@ struct Divide {
     // 2^-e in two factors: e = 127 has no float of its own.
     const float a = __uint_as_float(static_cast<uint32_t>(127 - (e >> 1)) << 23);
     const float b = __uint_as_float(static_cast<uint32_t>(127 - (e - (e >> 1))) << 23);
-    num = n * a * b;
+    // A negative earlier scale may be any multiple of the new one: from 2^20 on every
+    // code but 0 passes the format's largest alike.
+    num = fmaxf(n * a * b, -0x1p20f);
     den = d * a * b;
     inv = 1.f / den;
   }
@@ -127,7 +129,8 @@ struct Divide {
 // lies.  Cut toward zero, with the last bit set where anything was cut, it then
 // rounds to the format as the exact quotient would: no value of the format and
 // none half way between two has that bit.  kPair: x' does not fit one float (a
-// code times a scale), and is taken as two.
+// code times a scale), and is taken as two; an earlier scale may have been
+// negative, and the quotient then beyond INT8.
 template <int FMT, bool kPair>
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divide &by) {
   float q[8];
@@ -152,6 +155,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const Divide &by) {
       if (some && static_cast<int>(u ^ __float_as_uint(l[k])) < 0) --u;
       if (some) u |= 1u;
       q[i + k] = __uint_as_float(u);
+      if (kPair && FMT == ATTN_KV_INT8) q[i + k] = fminf(fmaxf(q[i + k], -128.f), 127.f);
     }
   }
   return make_uint2(codes4<FMT>(q), codes4<FMT>(q + 4));

@@ -56,3 +56,28 @@ def test_read_rounds_once(fmt, dtype):
             want = to_bf16(exact) if dtype == torch.bfloat16 else exact.astype(np.float32).astype(np.float64)
         assert np.array_equal(f64(k).reshape(P, -1), want)
         assert np.array_equal(f64(v).reshape(P, -1), -want)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("old", [-1.0, -0.013, -300.0, -3e38, -1e-40, 0.0, -0.0])
+def test_earlier_codes_under_a_negative_scale(fmt, old):
+    # A page whose scale was negative: its earlier codes change sign, and those that the new scale
+    # cannot hold become the format's largest.
+    d, Hkv = 64, 2
+    st = make([3], [9], Hkv, d, fmt, seed=31)
+    p = int(st["block_table"][0, 0])
+    for n in ("k", "v"):
+        st[n + "_scales"][p] = old
+    dv = on_gpu(st)
+    write(dv, fmt)
+    lo, hi = (-128.0, 127.0) if fmt == "int8" else (-448.0, 448.0)
+    for n in ("k", "v"):
+        new = np.maximum(np.abs(f64(st[n])).max((0, 2)).astype(np.float32) / np.float32(ref.QMAX[fmt]), np.float32(2.0 ** -126))
+        assert np.array_equal(f64(dv[n + "_scales"])[p], new.astype(np.float64))
+        was = ref.code_values(st[n + "_pages"], fmt)[p, :, :9]
+        x = was * float(np.float32(old)) / new.astype(np.float64)[:, None, None]
+        want = np.clip(np.rint(x), lo, hi) if fmt == "int8" else ref.nearest(x, fmt)
+        got = ref.code_values(dv[n + "_pages"], fmt)[p]
+        assert np.array_equal(got[:, :9], want)
+        rows = ref.nearest(f64(st[n]).transpose(1, 0, 2) / new.astype(np.float64)[:, None, None], fmt)
+        assert np.array_equal(got[:, 9:12], rows)
