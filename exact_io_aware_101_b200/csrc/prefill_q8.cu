@@ -1187,6 +1187,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       const bool use = ok && nt > 0 && l != 0.f;
       // O is relative to 2^(mv - kTop); in two factors, as that may be far from 1.
       const float part = ex2(0.5f * (mv - mm - kTop)), last = part * (poison ? NAN : 1.0f / sum);
+      // (A row that sees keys, and none with a score above -inf, is 0 / 0.)
+      const float unseen = !p.split && sum == 0.f ? NAN : 0.f;
       constexpr int kRow = D + 4;  // floats; keeps a store's eight lanes in different banks
       float *joint = reinterpret_cast<float *>(sRing + 8 * 32 * sizeof(float4));
       tc_fence_after();
@@ -1200,7 +1202,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         for (int i = 0; i < 32; i += 4) {
           float x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = use ? __uint_as_float(ov[i + k]) * part * last : 0.f;
+          for (int k = 0; k < 4; ++k) x[k] = use ? __uint_as_float(ov[i + k]) * part * last : unseen;
           dst[i >> 2] = make_float4(x[0], x[1], x[2], x[3]);
         }
       }
@@ -1266,6 +1268,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       tc_fence_after();
       const bool seen = l != 0.f;
       const float inv = poison ? NAN : (seen ? 1.0f / l : 0.f);
+      // (A row that sees keys, and none with a score above -inf, is 0 / 0.)
+      const float unseen = !p.split && !seen ? NAN : 0.f;
       const float l2 = seen ? m + log2f(l) : -INFINITY;
       // O is relative to 2^(mv - kTop); in two factors, as that may be far from 1.
       const float a0 = ex2(0.5f * (mv - m - kTop)), a1 = ex2(0.5f * (mv1 - m - kTop));
@@ -1281,7 +1285,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         // (A tile that has seen nothing may hold anything.)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          float x = use0 ? __uint_as_float(ov[i]) * a0 * b0 : 0.f;
+          float x = use0 ? __uint_as_float(ov[i]) * a0 * b0 : unseen;
           if constexpr (kTwin) x += use1 ? __uint_as_float(ov1[i]) * a1 * b1 : 0.f;
           ov[i] = __float_as_uint(x);
         }
@@ -1336,7 +1340,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_q8_join_kernel(const 
   const int at = (tok - pair * p.span) * p.heads + h - group * p.heads;
   const size_t slot = static_cast<size_t>(cta) * p.rows_cap + at;
   float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.l2_part[slot + static_cast<size_t>(i) * p.rows_cap]);
+  bool failed = false;
+  for (int i = lane; i < parts; i += 32) {
+    const float x = p.l2_part[slot + static_cast<size_t>(i) * p.rows_cap];
+    failed |= isnan(x);
+    top = fmaxf(top, x);
+  }
+  failed = __any_sync(0xffffffffu, failed);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   constexpr int E = D / 32;  // consecutive elements of this lane
@@ -1359,7 +1369,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill_q8_join_kernel(const 
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<uint32_t *>(p.o + row * D + lane * E + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
+  // (Scores that are all -inf: O is 0 / 0, and their log-sum-exp -inf.)
+  if (lane == 0) p.lse[row] = top == -INFINITY && !failed ? top : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // How a call is cut: query heads per CTA, tokens per tile and CTA, CTAs.

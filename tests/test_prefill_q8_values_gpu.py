@@ -181,3 +181,22 @@ def test_a_code_that_is_no_number_reaches_its_element_only(nq, copies, window):
         hit = (pos >= tok) & ((pos - window < tok) if window else True)
         nan[hit, :HQ // HKV, col] = True
     assert np.array_equal(np.isnan(f64(run(on_gpu(sick), fmt, window=window)[0])[:nq]), nan)
+
+
+@pytest.mark.parametrize("nq,copies", CUTS)
+def test_a_row_whose_scores_are_all_minus_infinity(nq, copies):
+    # K scales of infinity over negative codes: 0 / 0 by the formula, whichever way the call is cut;
+    # L is -inf, and the other heads' rows are what they were.
+    st = sequences(nq, 300, copies, "int8", seed=9)
+    st["q"] = st["q"].abs() + 0.5
+    st["k_pages"] = -st["k_pages"].abs().clamp(1, 127)
+    n = int(st["seq_lens"][0])
+    want = reference(st, "int8")
+    for b in range(-(-n // 16)):
+        st["k_scales"][int(st["block_table"][0, b]), 1] = float("inf")
+    o, lse = run(on_gpu(st), "int8")
+    assert o[:nq, HQ // HKV:].isnan().all()
+    assert (lse[:nq, HQ // HKV:] == float("-inf")).all()
+    own = (slice(None), slice(0, HQ // HKV))
+    # (Scores of one sign add up: their absolute sums reach 50, 2^-18 of which moves p and L.)
+    check(o, lse, want, rows=own, wide=2.0 ** -11)
