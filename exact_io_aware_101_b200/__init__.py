@@ -643,6 +643,12 @@ def _q8_types(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
                  block_table=block_table, seq_lens=seq_lens, cu_q=cu_q)
 
 
+def _bound(number, most: int) -> int:
+    """A count as a C int: what passes most (and changes nothing there) as most, anything negative
+    as -1, which the library refuses."""
+    return max(-1, min(int(number), most))
+
+
 _kv_write, _kv_read, _prefill_q8 = (_Call("attn_kv_write_paged_q8"), _Call("attn_kv_read_paged_q8"),
                                     _Call("attn_prefill_paged_q8"))
 _rope, _norm_rope, _norm_rope_bwd = (_Call("attn_rope"), _Call("attn_norm_rope"),
@@ -682,7 +688,7 @@ def attn_kv_write_paged_q8(k, v, k_pages, v_pages, k_scales, v_scales, block_tab
     _kv_write(index, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, k_pages.data_ptr(),
               v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), KV_FORMATS[kv_format],
               block_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), S, Hkv, T,
-              min(int(max_q), T), d, page_size, max_blocks, num_pages, _stream(k))
+              _bound(max_q, T), d, page_size, max_blocks, num_pages, _stream(k))
 
 
 def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
@@ -720,14 +726,14 @@ def attn_kv_read_paged_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq
     _kv_read(index, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
              v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
              seq_lens.data_ptr(), cu_q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPES[dtype], S,
-             Hkv, T, min(int(max_q), T), d, page_size, max_blocks, num_pages, _stream(k))
+             Hkv, T, _bound(max_q, T), d, page_size, max_blocks, num_pages, _stream(k))
     return k, v
 
 
 def prefill_q8_workspace_bytes(S: int, Hq: int, Hkv: int, T: int, max_q: int, d: int,
                                max_blocks: int, page_size: int = 16) -> int:
-    return int(library().attn_prefill_q8_workspace_bytes(S, Hq, Hkv, T, max_q, d, max_blocks,
-                                                         page_size))
+    return int(library().attn_prefill_q8_workspace_bytes(S, Hq, Hkv, T, _bound(max_q, T), d,
+                                                         max_blocks, page_size))
 
 
 def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q,
@@ -763,7 +769,7 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
     if alibi_slopes is not None:
         _check(alibi_slopes, "alibi_slopes", torch.float32, 1)
         slopes_ptr = alibi_slopes.data_ptr()
-    max_q = min(int(max_q), T)  # (no chunk is longer)
+    max_q = _bound(max_q, T)  # (no chunk is longer)
     need = prefill_q8_workspace_bytes(S, Hq, Hkv, T, max_q, d, max_blocks, page_size)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -774,8 +780,8 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
                 v_scales.data_ptr(), KV_FORMATS[kv_format], block_table.data_ptr(),
                 seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(), S, Hq, Hkv,
                 T, max_q, d, page_size, max_blocks, num_pages, float(scale),
-                min(int(window), 2**31 - 1),
-                slopes_ptr, workspace.data_ptr() if workspace is not None else None,
+                _bound(window, 2**31 - 1), slopes_ptr,
+                workspace.data_ptr() if workspace is not None else None,
                 workspace.numel() if workspace is not None else 0, _stream(q))
     return out, lse
 
