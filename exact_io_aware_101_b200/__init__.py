@@ -751,7 +751,7 @@ def attn_prefill_paged_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, 
         k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, cu_q, kv_format)
     _dims(q, "q", 3)
     T, Hq = q.shape[:2]
-    if q.shape[2] != d or Hq % Hkv != 0:
+    if q.shape[2] != d or Hkv == 0 or Hq % Hkv != 0:
         raise ValueError("q must be [T, Hq, d] with the pages' d and a multiple of their heads")
     _decode_out_dims(q, T, Hq, out, lse)
     if alibi_slopes is not None:

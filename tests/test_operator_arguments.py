@@ -21,6 +21,12 @@ def tensors(Hkv=2, device="cpu"):
                 cu_q=torch.tensor([0, 3], **i32))
 
 
+def test_pages_without_heads():
+    t = tensors(Hkv=0)
+    with pytest.raises(ValueError):
+        ea.attn_prefill_paged_q8(t["q"], *(t[n] for n in CACHE), max_q=3, kv_format="int8")
+
+
 # (Past the C int: -2^32 + 3 is 3 in 32 bits, and -2^32 is 0.)
 @pytest.mark.gpu
 @pytest.mark.parametrize("number", [-1, -2**31, -2**32, -2**32 + 3, -2**63])
