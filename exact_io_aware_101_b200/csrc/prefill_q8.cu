@@ -489,12 +489,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     je1 = jhi;
   }
   const int total = 2 * (jhi - jlo);  // K and V tiles of the walk
+  // The first page that a row sees: those before it may have been given back.
+  const int pg_first = p.window > 0 ? max(0, ck.ctx + tok0 - p.window + 1) / kPage : 0;
   // Twin tiles with at most a warp of rows: every quarter of a tile's lanes holds
   // all of them, and takes a quarter of its columns.
   const int rows_here = min(p.span, ck.nq - tok0) * p.heads;
   const bool few = kTwin && rows_here <= 32;
 
-  // ---- every page of those tiles must be in the pool.
+  // ---- every page of those tiles that a row sees must be in the pool.
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NST; ++i) {
       mbar_init(&sh->full[i], 128);
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
   {
     const int pg_end = min(jhi * kPagesPerTile, (ck.n + kPage - 1) / kPage);
     bool bad = false;
-    for (int i = jlo * kPagesPerTile + static_cast<int>(threadIdx.x); i < pg_end; i += NUM_THREADS) {
+    for (int i = max(jlo * kPagesPerTile, pg_first) + static_cast<int>(threadIdx.x); i < pg_end; i += NUM_THREADS) {
       const int pid = p.block_table[static_cast<size_t>(seq) * p.max_blocks + i];
       bad |= pid < 0 || pid >= p.num_pages;
     }
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
       int j, slot;
       entry<kTwin>(i, jlo, total, v, j, slot);
       const int pg = j * kPagesPerTile + 2 * w + (lane & 1);
-      return pg * kPage < ck.n ? table[pg] : -1;
+      return pg >= pg_first && pg * kPage < ck.n ? table[pg] : -1;
     };
     auto scales_of = [&](int i0, int pid) {
       bool v;
@@ -754,9 +756,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     int pid2 = -1;
     // Copies this lane's bytes of entry i of the round that `pids` is of into its
     // raw slot: only this lane reads them, so its own wait is all they need.
-    // Slots of pages behind the keys get zeros.  (Bulk copies of the 2 KB slices,
-    // by two warps of their own, went at 12.6 bytes a cycle and SM, and bounded
-    // calls of few rows: 73 us against 70 for 20 rows over 8 K to 32 K keys.)
+    // Slots of pages before or behind the keys get zeros.  (Bulk copies of the 2 KB
+    // slices, by two warps of their own, went at 12.6 bytes a cycle and SM, and
+    // bounded calls of few rows: 73 us against 70 for 20 rows over 8 K to 32 K keys.)
     auto copy = [&](int i, int pids) {
       if (i < total) {
         bool v;

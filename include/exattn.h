@@ -358,7 +358,8 @@ EXATTN_API attn_status_t attn_kv_read_paged_q8(
  * KV-cache quantisation).  Queries, chunks, window, ALiBi, outputs, errors and
  * bad pages as for attn_prefill_paged; pages, scales and kv_format as for
  * attn_decode_paged_q8 (the chunk's own tokens have been written, e.g. by
- * attn_kv_write_paged_q8).  Rows of no sequence stay as they are.
+ * attn_kv_write_paged_q8).  Entries of pages that lie behind the window of every
+ * row may name no page.  Rows of no sequence stay as they are.
  * A code of V that is NaN makes its element of O NaN in the rows that see its
  * token, and a V scale that is not finite every element in the rows that see a
  * token of its page; nothing else changes.

@@ -200,3 +200,20 @@ def test_a_row_whose_scores_are_all_minus_infinity(nq, copies):
     own = (slice(None), slice(0, HQ // HKV))
     # (Scores of one sign add up: their absolute sums reach 50, 2^-18 of which moves p and L.)
     check(o, lse, want, rows=own, wide=2.0 ** -11)
+
+
+@pytest.mark.parametrize("nq,copies", CUTS)
+@pytest.mark.parametrize("window", [1, 40, 130])
+def test_pages_given_back_behind_the_window(nq, copies, window):
+    # Pages that end before the first key that any row sees are no longer the sequence's: their
+    # entries name no page, and are not looked at.
+    ctx = 600
+    st = sequences(nq, ctx, copies, "e4m3", seed=11)
+    want = reference(st, "e4m3", window)
+    st["block_table"][0, :(ctx - window + 1) // 16] = -1
+    check(*run(on_gpu(st), "e4m3", window=window), want)
+    assert ea.device_status(clear=True) == 0
+    st["block_table"][0, (ctx - window + 1) // 16] = -1  # the first that is seen
+    o, _ = run(on_gpu(st), "e4m3", window=window)
+    assert ea.device_status(clear=True) == ea.ATTN_DEV_BAD_PAGE
+    assert o[0].isnan().all() and o[nq:].isfinite().all()
