@@ -96,13 +96,8 @@ __device__ __forceinline__ void values4(uint32_t w, float *v) {
     // 2^23 + code + 128.
     const uint32_t b = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const float2 x = add2(make_float2(__uint_as_float(prmt(b, 0x4b000000u, 0x7440u | i)),
-                                        __uint_as_float(prmt(b, 0x4b000000u, 0x7441u | i))),
-                            make_float2(-8388736.f, -8388736.f));
-      v[i] = x.x;
-      v[i + 1] = x.y;
-    }
+    for (int i = 0; i < 4; ++i)
+      v[i] = __uint_as_float(prmt(b, 0x4b000000u, 0x7440u | i)) - 8388736.f;
   }
 }
 
@@ -308,15 +303,20 @@ struct ReadParams {
   int Hkv, T, max_q, max_blocks, num_pages, pages_per_seq, parts;
 };
 
-// x * y for a rounding to bf16 as of the exact product: of the two float32 values
-// around it the one whose last bit is set.  Neither a bf16 value nor one half way
-// between two has that bit, so none lies between the result and the product.  (Rounded
-// to float32 first, a product next to a tie lands on it: 27 of 4 million INT8 ones.
-// This took reading all 64 sequences from 281 to 282 us, over INT8 from 289 to 302;
-// looking for ties first 360, the sign of the product's remainder 331.)
-__device__ __forceinline__ float mul_odd(float x, float y) {
-  const float below = __fmul_rd(x, y), above = __fmul_ru(x, y);
-  return __float_as_uint(below) & 1u ? below : above;
+// A code times a scale, for a rounding to bf16 as of the exact product.  (Rounded to
+// float32 first, a product next to a tie lands on it: 27 of 4 million INT8 ones.)
+// A scale of at most 9 bits, trailing zeros aside, has products of at most 17, which
+// float32 holds (but for some below 2^-136, which are zeros in bf16 either way).  The
+// products of a longer scale are longer than 9 bits too, and so none of them is a
+// bf16 value or half way between two: cut toward zero and with the last bit set,
+// they lie on the same side of all of those.  (Reading 64 sequences of up to 8192
+// tokens: E4M3 281 us as before, INT8 293 instead of 289.  Of the two float32 values
+// around each product the one with the last bit set: 282 and 302, and in a run of
+// calls 303 against 285.)
+__device__ __forceinline__ uint32_t last_bit(float scale) {
+  const uint32_t u = __float_as_uint(scale) & 0x7fffffffu;
+  const uint32_t digits = (u & 0x7fffffu) | (u >= 0x800000u ? 0x800000u : 0u);
+  return 32 - __clz(digits) - (__ffs(digits) - 1) > 9 ? 1u : 0u;
 }
 
 __device__ __forceinline__ void store4(float *p, const float *v) {
@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadParams p
     }
   }
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint32_t last = last_bit(scale[kv]);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int r = i * RPP + row;
@@ -369,7 +370,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadParams p
       values4<FMT>(in[kv][i].x, v);
       values4<FMT>(in[kv][i].y, v + 4);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = sizeof(T) == 2 ? mul_odd(v[e], scale[kv]) : v[e] * scale[kv];
+      for (int e = 0; e < 8; ++e)
+        v[e] = sizeof(T) == 2 ? __uint_as_float(__float_as_uint(__fmul_rz(v[e], scale[kv])) | last) : v[e] * scale[kv];
       T *out = static_cast<T *>(p.out[kv]) +
                ((c.q0 + static_cast<long long>(page) * kPage - c.ctx + r) * p.Hkv + head) * D + col;
       if constexpr (sizeof(T) == 2) {
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadParams p
         store4(out + 4, v + 4);
       }
     }
+  }
 }
 
 // Pages a chunk of at most max_q tokens can touch: one token touches one, and
