@@ -796,8 +796,11 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     positions are interpolated); "ntk" raises the base so that the slowest pair
     alone is divided by factor and the fastest keeps its pace; "yarn" keeps pairs
     that turn at least beta_fast times over the original length, divides those
-    that turn at most beta_slow times, blends in between, and asks for the
-    attention factor 0.1 ln(factor) + 1.
+    that turn at most beta_slow times, blends in between, linearly in the number
+    of turns, and asks for the attention factor 0.1 ln(factor) + 1.  That is the
+    method as its paper defines it.  Models trained with a blend that is linear in
+    the pair's index, between two rounded indices, have other frequencies for the
+    pairs in between: give the calls those as inv_freq.
     """
     if rot < 2 or rot % 2:
         raise ValueError("rot must be even and at least 2")
