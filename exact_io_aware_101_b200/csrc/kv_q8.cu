@@ -34,7 +34,7 @@
 // d = 128): writing 16 x 512 tokens 13 us (INT8) and 14.5 us (E4M3), 3.8 and 3.5
 // TB/s of bf16 in and codes out, a third of it start and end; 16 x 4096 tokens 79
 // us, 5.1 TB/s; 64 sequences' one token 3.2 us; reading 64 sequences of up to 8192
-// tokens as bf16 279 us, 6.5 TB/s (99 % of the measured copy rate).  One warp takes one
+// tokens as bf16 281 us, 6.4 TB/s (98 % of the measured copy rate).  One warp takes one
 // slice (write: of K or of V; read: of both), so no two warps share a scale
 // and a slice's maximum is one warp reduction; a lane moves 16-byte words of
 // bf16 and has the slice's whole share (at most 8 of them) in flight.  Earlier

@@ -23,14 +23,21 @@
 //                   128-byte-swizzled layout that the MMAs read;
 //      warps 8-11   softmax, correction and epilogue of tile 0, warps 12-15 of
 //                   tile 1; before that they bring the tiles' queries to f16.
-//  * What bounds it, and what it measured (B200, E4M3, d = 128, 32 query and 8 K/V
-//    heads).  16 chunks of 512 tokens after up to 7680: the chain of a row tile,
-//    product -> softmax -> product, 3600 cycles a key tile against the tensor
-//    cores' 2048; 560 us, 949 TFLOP/s or 58 % of the measured bf16 rate, and 600
-//    us in a run long enough for the power limit.  Four sequences of five tokens
-//    (20 rows a K/V head) over 8 K to 32 K keys, INT8: the widening, about 900
-//    cycles a tile, beside some 10 us of launches, plan and joining; 70 us, 2.5
-//    TB/s of codes or 39 % of the measured copy rate.
+//  * What bounds it, and what it measured (B200, d = 128, 32 query and 8 K/V heads;
+//    cycles by timestamps in the kernel).  16 chunks of 512 tokens after up to 7680,
+//    E4M3: 567 us, 938 TFLOP/s or 58 % of the measured bf16 rate, with the SMs at
+//    1.81 GHz; 606 us at 1.70 GHz, in a run long enough for the power limit.  An SM
+//    has seven CTAs one after another and 219 key tiles.  A key tile takes 3870
+//    cycles, in which the tensor cores work 2048, the widening warps all but the 490
+//    that they wait for free slots, and a row tile's softmax all but the 820 that it
+//    waits for scores: 85 % of the time.  A CTA's start and end take 22600 (4500 for
+//    its pages, 11100 for the queries and the first scores, 7000 for the last product
+//    and the rows): 15 %.
+//    Four sequences of five tokens (20 rows a K/V head) over 8 K to 32 K keys, INT8:
+//    72 us, 2.5 TB/s of codes or 38 % of the measured copy rate, at 1.82 GHz.  The
+//    longest CTA has 39 key tiles of 2320 cycles, 1160 each for K and V, of which the
+//    widening warps wait 130 for a slot: widening is what bounds them.  50 us, and
+//    11 us for the CTA's plan, start and end; the rest is launches and the joining.
 //  * Exactness.  Codes are exact in f16.  Queries are scaled by a power of two
 //    per row before rounding to f16, exact for elements within 2^28 of the
 //    row's largest.  The K scale multiplies the f32 scores, per page.  The V
@@ -704,9 +711,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
     };
     // A lane's share of a raw tile, unscaled.  The compiler keeps loads and stores
     // of shared memory in order, so that one load at a time waits for the store
-    // before it (900 cycles a tile); twin tiles, where this is what bounds the
-    // kernel, load all of it first (700; beside two busy softmaxes that gains
-    // nothing: 560 us against 549 for 16 chunks of 512).
+    // before it; twin tiles, where this is what bounds the kernel, load all of it
+    // first (200 of 900 cycles a tile less when it was brought in; beside two busy
+    // softmaxes that gained nothing: 560 us against 549 for 16 chunks of 512).
     auto widen = [&](const uint8_t *src, uint8_t *dst) {
       constexpr int A = kTwin ? 2 * PASSES : 1;
 #pragma unroll

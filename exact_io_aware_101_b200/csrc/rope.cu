@@ -16,7 +16,10 @@
 // elements.  Measured (B200): norm and rotation of 4 x 4096 tokens of 40 bf16
 // heads, d = 128, 56 us (6.0 TB/s, 92 % of the measured copy rate), its gradient
 // 89 us (5.7 TB/s, 87 %), a partial fp32 rotation of 2 x 2047 tokens of 32
-// heads, d = 64, 11.0 us (6.2 TB/s), one decode step of 64 tokens 3.3 us.  So:
+// heads, d = 64, 11.0 us (6.2 TB/s), one decode step of 64 tokens 3.3 us, the bare
+// bf16 turn of the 4 x 4096 tokens 59 us (5.6 TB/s; interleaved 60).  Half layouts
+// that go element by element (below) take twice that: 121 us for 90 of 128 turned,
+// 124 with a norm, 207 for its gradient.  So:
 //  * One thread holds the same 16 elements (8 pairs) of its rows and walks the
 //    heads of one token, q's and then k's: the cosines and sines of its 8 pairs
 //    stay in registers, worked out once for all those heads.  LPR = d/16 lanes
@@ -246,10 +249,13 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Blocks that an SM holds at a time (the registers' limit is set to that; one more
-// spills), and rows on their way while one is worked on.  The norms' rows wait in
-// shared memory, where words lie as they do in global memory; a bare turn, which
-// has registers to spare, and layouts of single elements hold theirs in registers.
+// Blocks that an SM holds at a time (the registers' limit is set to that), and rows
+// on their way while one is worked on.  One block more takes 63 us instead of 56 for
+// the norm and 111 instead of 89 for its gradient.  At these limits the bf16 kernels
+// spill a little in some layouts: the bare turn 20 bytes (halves) and 40
+// (interleaved), single elements 56 with a norm and 76 in its gradient.  The norms'
+// rows wait in shared memory, where words lie as they do in global memory; bare turns
+// and layouts of single elements hold theirs in registers.
 // (In registers: 60 us for the norm and 100 for its gradient instead of 56 and 89,
 // 4 x 4096 tokens of 40 bf16 heads.  Staged: 11.4 us for the fp32 turn of 2 x 2047
 // tokens instead of 11.0.)

@@ -443,7 +443,7 @@ EXATTN_API attn_status_t attn_norm_rope(
  *   dq_weight, dk_weight   [d] float32 (out)
  *   workspace    device scratch of at least attn_norm_rope_bwd_workspace_bytes(B,
  *                Hq, Hkv, N, d) bytes, owned by the caller; no initialisation
- *                needed
+ *                needed.  Calls that may run at the same time need one each.
  * The result is deterministic: no atomics.  With B == 0 or N == 0 the weights'
  * gradients are 0.
  */
