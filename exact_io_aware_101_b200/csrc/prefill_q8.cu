@@ -1237,9 +1237,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         if (!p.split) p.lse[out_row] = l2 * 0.6931471805599453f;
         else p.l2_part[static_cast<size_t>(lin) * p.rows_cap + lane] = l2;
       }
-      if (FMT == ATTN_KV_E4M3 && *reinterpret_cast<volatile int *>(&sh->any_bad)) {
-        soft_barrier();  // the rows are stored
-        if (me == 0 && valid) spoil(tok, p.split ? static_cast<size_t>(lin) * p.rows_cap + lane : out_row);
+      if (FMT == ATTN_KV_E4M3) {
+        // The rows are stored.  (Every warp takes the barrier: after a wait that ran
+        // out the flag may still change, and they may read it differently.)
+        soft_barrier();
+        if (me == 0 && valid && *reinterpret_cast<volatile int *>(&sh->any_bad))
+          spoil(tok, p.split ? static_cast<size_t>(lin) * p.rows_cap + lane : out_row);
       }
       ok = false;  // nothing more for these warps
     }
