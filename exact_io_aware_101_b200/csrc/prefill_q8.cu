@@ -275,15 +275,20 @@ __device__ __forceinline__ float scale_log2(float v) {
 }
 // Weights of N pages against a row's references, from their V scales v; visible
 // columns [lo, hi).  Where a scale is no number its page weighs nothing and a row
-// that sees it is poisoned.  A weight beyond float32 becomes its largest: P is 0 in
-// float32 there, or the reference would have moved.  (Without a branch: one around
-// the rare part cost 2 % of the time of 16 chunks of 512.)
+// that sees it is poisoned.  A weight may be as large as P is small (their product is
+// 2^12 at most, or the reference would have moved): both are taken from the middle of
+// float32's range, weights 2^-kLift times and P 2^kLift times as large.  One that is
+// still beyond float32 becomes its largest: its P is below 2^-176 of the row's
+// largest.  (Without a branch: one around the rare part cost 2 % of the time of 16
+// chunks of 512.)
+constexpr float kLift = 60.f;
 template <int N>
 __device__ __forceinline__ void weigh(float (&v)[N], float h, int lo, int hi, bool &poison) {
   const float2 h2 = make_float2(h, h), z2 = make_float2(0.f, 0.f);
+  const float2 low2 = make_float2(h * 0x1p-60f, h * 0x1p-60f);  // first: v h may overflow
 #pragma unroll
   for (int g = 0; g < N; g += 2) {
-    const float2 x = fma2(fma2(make_float2(v[g], v[g + 1]), h2, z2), h2, z2);
+    const float2 x = fma2(fma2(make_float2(v[g], v[g + 1]), low2, z2), h2, z2);
     const float w[2] = {x.x, x.y};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -968,7 +973,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         float vp[2] = {vs.x, vs.y};
         weigh(vp, half_weight(m, mv), lo, hi, poison);
         const float ones[2] = {1.f, 1.f};
-        l += exp_cols(sv, ones, vp, m == -INFINITY ? 0.f : m, pk);
+        l = fmaf(exp_cols(sv, ones, vp, (m == -INFINITY ? 0.f : m) - kLift, pk), 0x1p-60f, l);
         const uint32_t zero[16] = {};
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -1133,7 +1138,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) prefill_q8_kernel(const Params
         float vp[4];
         four(&sh->v_scale[slot][4 * hf], vp);
         weigh(vp, h, lo - 64 * hf, hi - 64 * hf, poison);
-        l += exp_cols(sv, ones, vp, m_use, pk);
+        l = fmaf(exp_cols(sv, ones, vp, m_use - kLift, pk), 0x1p-60f, l);
         store_half(s_addr + 32 * hf, pk);
         tmem_st_wait();
         tc_fence_before();

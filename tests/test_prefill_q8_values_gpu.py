@@ -217,3 +217,23 @@ def test_pages_given_back_behind_the_window(nq, copies, window):
     o, _ = run(on_gpu(st), "e4m3", window=window)
     assert ea.device_status(clear=True) == ea.ATTN_DEV_BAD_PAGE
     assert o[0].isnan().all() and o[nq:].isfinite().all()
+
+
+@pytest.mark.parametrize("nq,copies", CUTS)
+@pytest.mark.parametrize("far", [116, 122, 128])
+def test_a_weight_at_the_end_of_float32(nq, copies, far):
+    # One page's keys score 84 below the others' (2^-122 of their weight) and hold values 2^far times
+    # theirs: a sixty-fourth of the sum, as much as the others, 64 times as much.
+    n = 16 * 40
+    st = sequences(nq, n - nq, copies, "e4m3", seed=far)
+    st["v_scales"] *= 2.0 ** -60
+    st["q"][..., 0] = 8.0
+    st["k_pages"].view(torch.uint8)[..., 0] = 0
+    p = int(st["block_table"][0, 17])
+    st["k_pages"][p] = torch.zeros_like(st["k_pages"][p])
+    st["k_pages"][p, :, :, 0] = torch.full((HKV, 16), -112.0).to(st["k_pages"].dtype)
+    st["k_scales"][p] = 0.75
+    st["v_scales"][p] *= 2.0 ** (far // 2)
+    st["v_scales"][p] *= 2.0 ** (far // 2)
+    # (Scores of 84 are off by 2^-18 of that, which moves p and the row sum.)
+    check(*run(on_gpu(st), "e4m3"), reference(st, "e4m3"), wide=2.0 ** -10.6)
