@@ -48,7 +48,7 @@
 //    that largest one lose bits, 2^-29 of it at most.  Relative to the largest V
 //    scale of the CTA's pages, one later large value took the bits of every row
 //    before it; that took 561 us for the 16 chunks above, 945 with ALiBi and 481
-//    with d = 64, this 567, 952 and 485.  Scaling the codes on their way
+//    with d = 64, this 566, 949 and 487.  Scaling the codes on their way
 //    costs two roundings, and as much time.)
 //  * Few rows and long keys.  A chunk that fits one row tile gives both tiles the
 //    same rows and half of the CTA's keys each ("twin"), which overlaps what one
